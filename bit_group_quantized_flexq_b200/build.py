@@ -10,11 +10,12 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "flexq_api.cu")
+SRC = os.path.join(PKG, "csrc", "flexq_lib.cu")
 LIB = os.path.join(PKG, "libflexq.so")
 DEPS = [os.path.join(PKG, "csrc", f) for f in
-        ("flexq_api.cu", "flexq_gemm.cuh", "flexq_gemm_wide.cuh", "flexq_quant.cuh",
-                  "flexq_ptx.cuh")] + \
+        ("flexq_lib.cu", "flexq_api.cu", "flexq_gemm.cuh", "flexq_gemm_wide.cuh",
+         "flexq_quant.cuh", "flexq_ptx.cuh", "flexq_w4.cuh", "flexq_embed.cuh",
+         "flexq_w4_api.cuh")] + \
        [os.path.join(ROOT, "include", "flexq.h")]
 
 NVCC_FLAGS = [

@@ -1,0 +1,369 @@
+// flexq_embed.cuh -- rows of a packed weight table: lookup with scaling, and
+// its gradient by sorted tokens.
+//
+//   y[t,k]  = a * q[id_t,k] * s[id_t, k / gs]
+//   D[v,k]  = a * sum over t with id_t = v of dy[t,k]   (in the order of t)
+//   ds[v,g] = sum over k in g of D[v,k] * q[v,k]
+//
+// The codes are constants; D is the gradient of the rows of a latent table
+// whose rounding is passed through, ds the exact gradient of the scales.  A
+// token outside [0, V) is padding: a zero row, and no gradient.  Tables are
+// in the 4-bit form of flexq_w4.cuh (scales [V, G]) or in the byte-aligned
+// 6-bit form of flexq_quant.cuh (scales [G, V]).
+#pragma once
+
+#include "flexq_w4.cuh"
+
+namespace flexq {
+
+struct Table {
+  const uint8_t* packed;
+  const __half* scales;
+  int V, K, G, kbs, gs_shift;       // kbs: tiles of 128 columns, gs = 1 << gs_shift
+};
+
+// The word i (0..2) of 16-code block b (0..7) of a row of a 6-bit table.
+__device__ __forceinline__ uint32_t w6_block_word(const uint8_t* packed, int v, int kb, int kbs, int b,
+                                                  int i) {
+  const int o = 12 * b + 4 * i;
+  return __ldg(reinterpret_cast<const uint32_t*>(
+      packed + (static_cast<size_t>(v >> 7) * kbs + kb) * 12288 +
+      static_cast<size_t>((o >> 4) * 128 + (v & 127)) * 16 + (o & 15)));
+}
+
+// The codes of columns k .. k+7 (k % 8 == 0) of row v.
+template <int BITS>
+__device__ __forceinline__ void table_codes8(const Table& tb, int v, int k, int (&q)[8]) {
+  if (BITS == 4) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tb.packed + w4_word_offset(v, k, tb.kbs)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = w4_code(w, i);
+  } else {
+    // byte t of word i holds code 4 i + t in bits [7:2] and bits [2i+1:2i] of
+    // code 12 + t in bits [1:0]
+    const int kb = k >> 7, b = (k >> 4) & 7;
+    uint32_t w[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) w[i] = w6_block_word(tb.packed, v, kb, tb.kbs, b, i);
+    const bool upper = k & 8;
+    const uint32_t first = upper ? w[2] : w[0];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      q[t] = static_cast<int8_t>(first >> (8 * t)) >> 2;
+      const uint32_t u = ((w[0] >> (8 * t)) & 3u) | ((w[1] >> (8 * t)) & 3u) << 2 | ((w[2] >> (8 * t)) & 3u) << 4;
+      const int last = static_cast<int>(u << 26) >> 26;
+      q[4 + t] = upper ? last : static_cast<int8_t>(w[1] >> (8 * t)) >> 2;
+    }
+  }
+}
+
+template <int BITS>
+__device__ __forceinline__ size_t scale_index(const Table& tb, int v, int grp) {
+  return BITS == 4 ? static_cast<size_t>(v) * tb.G + grp : static_cast<size_t>(grp) * tb.V + v;
+}
+
+// The token's row, or -1 for padding.
+__device__ __forceinline__ int token_row(const void* ids, int id_bytes, long long t, int V) {
+  const long long id = id_bytes == 8 ? __ldg(static_cast<const long long*>(ids) + t)
+                                     : __ldg(static_cast<const int*>(ids) + t);
+  return id >= 0 && id < V ? static_cast<int>(id) : -1;
+}
+
+// ------------------------------------------------------------------ lookup --
+// One thread per eight columns of a token: consecutive threads write
+// consecutive 16-byte pieces of a row.
+template <typename T, int BITS>
+__global__ void __launch_bounds__(256) embed_kernel(const Table tb, const void* __restrict__ ids,
+                                                    int id_bytes, long long units, float scale,
+                                                    T* __restrict__ out) {
+  const int per_row = tb.K >> 3;
+  for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < units;
+       u += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const long long tok = u / per_row;
+    const int k = static_cast<int>(u - tok * per_row) * 8;
+    const int v = token_row(ids, id_bytes, tok, tb.V);
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (v >= 0) {
+      int q[8];
+      table_codes8<BITS>(tb, v, k, q);
+      const float s = __half2float(__ldg(tb.scales + scale_index<BITS>(tb, v, k >> tb.gs_shift)));
+      uint32_t* p = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)        // code * scale is exact in FP32
+        p[i] = Elem<T>::pack(static_cast<float>(q[2 * i]) * s * scale,
+                             static_cast<float>(q[2 * i + 1]) * s * scale);
+    }
+    *reinterpret_cast<uint4*>(out + tok * tb.K + k) = o;
+  }
+}
+
+// -------------------------------------------------------------------- sort --
+// Tokens sorted by row, equal rows in the order of the tokens (stable), by a
+// least-significant-digit radix sort of 8-bit digits.  One cluster sorts;
+// its CTAs exchange digit counts in distributed shared memory and meet at
+// the cluster's barrier, so that one launch does every pass.  The grid's
+// other clusters meanwhile zero the outputs.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortDigits = 256;
+
+struct SortArgs {
+  const void* ids;
+  int id_bytes;
+  int T, V, passes;
+  uint2* buf[2];                  // (row, token); padding has row V
+  uint4* fill[2];                 // outputs to zero, in 16-byte pieces, and their ends
+  long long fill_n[2];
+  float* tail;                    // the last 0..3 floats of the second output
+  int tail_n;
+  int clusters_size;              // CTAs of the sorting cluster
+};
+
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs a) {
+  __shared__ unsigned hist[kSortWarps][kSortDigits];
+  __shared__ unsigned total[kSortDigits];
+  __shared__ unsigned base[kSortDigits];
+  __shared__ unsigned warp_sum[kSortDigits / 32];
+  const int C = a.clusters_size;
+  if (static_cast<int>(blockIdx.x) >= C) {
+    const long long stride = static_cast<long long>(gridDim.x - C) * kSortThreads;
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      for (long long i = static_cast<long long>(blockIdx.x - C) * kSortThreads + threadIdx.x;
+           i < a.fill_n[f]; i += stride)
+        a.fill[f][i] = make_uint4(0, 0, 0, 0);
+    if (static_cast<int>(blockIdx.x) == C && static_cast<int>(threadIdx.x) < a.tail_n)
+      a.tail[threadIdx.x] = 0.0f;
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1u;
+  const int rank = blockIdx.x;
+  // each warp owns a run of consecutive tokens
+  const long long per_warp = ((static_cast<long long>(a.T) + kSortWarps * C - 1) / (kSortWarps * C) + 31) / 32 * 32;
+  const long long lo = min(static_cast<long long>(a.T), (static_cast<long long>(rank) * kSortWarps + warp) * per_warp);
+  const long long hi = min(static_cast<long long>(a.T), lo + per_warp);
+
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = 8 * pass;
+    const uint2* src = a.buf[(pass + 1) & 1];
+    uint2* dst = a.buf[pass & 1];
+    auto item = [&](long long i) {
+      if (pass == 0) {
+        const int v = token_row(a.ids, a.id_bytes, i, a.V);
+        return make_uint2(v < 0 ? a.V : v, static_cast<unsigned>(i));
+      }
+      return __ldcg(src + i);
+    };
+    for (int i = lane; i < kSortDigits; i += 32) hist[warp][i] = 0;
+    __syncwarp();
+    for (long long i0 = lo; i0 < hi; i0 += 32) {
+      const bool in = i0 + lane < hi;
+      const unsigned d = in ? (item(i0 + lane).x >> shift) & 255u : 256u;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+      if (in && (same & below) == 0) hist[warp][d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (threadIdx.x < kSortDigits) {           // each warp's first place within the CTA
+      unsigned sum = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const unsigned c = hist[w][threadIdx.x];
+        hist[w][threadIdx.x] = sum;
+        sum += c;
+      }
+      total[threadIdx.x] = sum;
+    }
+    if (C > 1) cluster_sync_all(); else __syncthreads();
+    unsigned all = 0, before = 0, incl = 0;
+    if (threadIdx.x < kSortDigits) {
+      for (int r = 0; r < C; ++r) {
+        unsigned c;
+        if (C > 1)
+          asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                       : "=r"(c) : "r"(map_to_rank(smem_u32(&total[threadIdx.x]), r)) : "memory");
+        else
+          c = total[threadIdx.x];
+        all += c;
+        if (r < rank) before += c;
+      }
+      incl = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+    }
+    __syncthreads();
+    if (threadIdx.x < kSortDigits) {
+      unsigned low = 0;
+      for (int w = 0; w < warp; ++w) low += warp_sum[w];
+      base[threadIdx.x] = low + incl - all + before;
+    }
+    __syncthreads();
+    for (long long i0 = lo; i0 < hi; i0 += 32) {
+      const bool in = i0 + lane < hi;
+      const uint2 it = in ? item(i0 + lane) : make_uint2(0, 0);
+      const unsigned d = in ? (it.x >> shift) & 255u : 256u;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+      const unsigned at = in ? hist[warp][d] : 0;
+      __syncwarp();
+      if (in) {
+        dst[base[d] + at + __popc(same & below)] = it;
+        if ((same & below) == 0) hist[warp][d] = at + __popc(same);
+      }
+      __syncwarp();
+    }
+    // the next pass reads what every CTA of the cluster wrote, and none
+    // clears its counts while another reads them
+    if (C > 1) cluster_sync_all(); else __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------------- sums --
+constexpr int kSumThreads = 256;
+constexpr int kSumCols = kSumThreads * 8;
+constexpr int kSumMaxTile = 64;
+
+struct SumArgs {
+  const uint2* sorted;
+  const void* dy;
+  int T, tile;                    // sorted tokens per CTA
+  float scale;
+  float* partial;                 // [tiles][2][K]: a tile's part of a run it shares with others
+  void* table;                    // row gradient, or null
+  float* scales;                  // scale gradient, or null
+};
+
+// Writes the finished sums of columns k .. k+7 of row v.  All threads of a
+// warp take part (the group sums are shuffles); `in` says whose columns exist.
+template <typename T, typename TO, int BITS>
+__device__ __forceinline__ void embed_finish(const Table& tb, const SumArgs& a, int v, int k, bool in,
+                                             const float (&acc)[8]) {
+  float d[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d[i] = acc[i] * a.scale;
+  if (a.table && in) {
+    TO* row = static_cast<TO*>(a.table) + static_cast<size_t>(v) * tb.K + k;
+    if constexpr (sizeof(TO) == 4) {
+      reinterpret_cast<float4*>(row)[0] = make_float4(d[0], d[1], d[2], d[3]);
+      reinterpret_cast<float4*>(row)[1] = make_float4(d[4], d[5], d[6], d[7]);
+    } else {
+      uint4 o;
+      o.x = Elem<T>::pack(d[0], d[1]);
+      o.y = Elem<T>::pack(d[2], d[3]);
+      o.z = Elem<T>::pack(d[4], d[5]);
+      o.w = Elem<T>::pack(d[6], d[7]);
+      *reinterpret_cast<uint4*>(row) = o;
+    }
+  }
+  if (a.scales) {
+    float sum = 0.0f;
+    if (in) {
+      int q[8];
+      table_codes8<BITS>(tb, v, k, q);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(d[i], static_cast<float>(q[i]), sum);
+    }
+    const int lanes = 1 << (tb.gs_shift - 3);         // threads per group: 4 .. 32
+    for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (in && (k & ((1 << tb.gs_shift) - 1)) == 0)
+      a.scales[scale_index<BITS>(tb, v, k >> tb.gs_shift)] = sum;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void add8(float (&acc)[8], const uint4& x) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Elem<T>::unpack(p[i]);
+    acc[2 * i] += f.x;
+    acc[2 * i + 1] += f.y;
+  }
+}
+
+// One CTA: a tile of consecutive sorted tokens, 2048 columns.  Runs of equal
+// rows inside the tile are finished here; what a run has in a tile that it
+// shares with others goes to `partial` and is joined by embed_join_kernel, so
+// that a row with many tokens is spread over many CTAs and every sum has one
+// fixed order.
+template <typename T, typename TO, int BITS>
+__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, const SumArgs a) {
+  __shared__ uint2 items[kSumMaxTile + 2];            // with the neighbours on both sides
+  const long long p0 = static_cast<long long>(blockIdx.x) * a.tile;
+  const int n = static_cast<int>(min(static_cast<long long>(a.tile), a.T - p0));
+  for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
+    const long long p = p0 + i - 1;
+    items[i] = p >= 0 && p < a.T ? a.sorted[p] : make_uint2(0xFFFFFFFFu, 0);
+  }
+  __syncthreads();
+  const int k = blockIdx.y * kSumCols + threadIdx.x * 8;
+  const bool in = k < tb.K;
+  const T* dy = static_cast<const T*>(a.dy);
+  constexpr int kAhead = 8;                           // loads in flight per thread
+  float acc[8] = {};
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    uint4 x[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (in && i0 + j < n && items[1 + i0 + j].x < static_cast<unsigned>(tb.V))
+        x[j] = __ldcs(reinterpret_cast<const uint4*>(dy + static_cast<size_t>(items[1 + i0 + j].y) * tb.K + k));
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j;
+      if (i >= n) break;
+      const unsigned v = items[1 + i].x;
+      if (v >= static_cast<unsigned>(tb.V)) return;   // padding sorts last
+      if (in) add8<T>(acc, x[j]);
+      if (i + 1 < n && items[2 + i].x == v) continue; // the run goes on in this tile
+      const bool first_run = v == items[1].x;
+      const bool shared_before = first_run && items[0].x == v;
+      const bool shared_after = i + 1 == n && items[2 + i].x == v;
+      if (shared_before || shared_after) {
+        if (in) {
+          float4* p = reinterpret_cast<float4*>(
+              a.partial + (static_cast<size_t>(blockIdx.x) * 2 + (shared_before ? 0 : 1)) * tb.K + k);
+          p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        }
+      } else {
+        embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc);
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+    }
+  }
+}
+
+// Joins the run that starts in tile blockIdx.x and goes on into the next.
+template <typename T, typename TO, int BITS>
+__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const Table tb, const SumArgs a) {
+  const long long end = (static_cast<long long>(blockIdx.x) + 1) * a.tile;   // of the tile
+  if (end >= a.T) return;
+  const unsigned v = a.sorted[end - 1].x;
+  if (v >= static_cast<unsigned>(tb.V) || a.sorted[end].x != v) return;
+  const long long begin = end - a.tile;
+  if (begin > 0 && a.sorted[begin].x == v && a.sorted[begin - 1].x == v) return;   // starts earlier
+  const int k = blockIdx.y * kSumCols + threadIdx.x * 8;
+  const bool in = k < tb.K;
+  float acc[8] = {};
+  auto add = [&](size_t slot) {
+    if (!in) return;
+    const float4* p = reinterpret_cast<const float4*>(a.partial + slot * tb.K + k);
+    const float4 x = p[0], y = p[1];
+    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+    acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+  };
+  size_t tile = blockIdx.x;
+  add(tile * 2 + 1);
+  for (long long e = end;; e += a.tile) {             // tiles that begin with v
+    ++tile;
+    add(tile * 2);
+    if (e + a.tile >= a.T || a.sorted[e + a.tile - 1].x != v || a.sorted[e + a.tile].x != v) break;
+  }
+  embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc);
+}
+
+}  // namespace flexq

@@ -1,0 +1,384 @@
+// flexq_w4_api.cuh -- host side of the 4-bit linear layers and of the packed
+// table's lookup and gradient: argument checks, launch shapes, launches.
+#pragma once
+
+#include "flexq_embed.cuh"
+#include "flexq_w4.cuh"
+
+namespace {
+
+int log2_gs(int gs) { return gs == 32 ? 5 : gs == 64 ? 6 : gs == 128 ? 7 : 8; }
+
+// Shapes of the 4-bit form: any N; K a multiple of the group size.
+int check_w4_shape(int N, int K, int gs) {
+  if (N <= 0 || K <= 0) return fail(FLEXQ_ERR_INVALID_ARG, "sizes must be N > 0, K > 0 (N=%d K=%d)", N, K);
+  if (!valid_gs(gs)) return fail(FLEXQ_ERR_UNSUPPORTED, "group_size %d not in {32,64,128,256}", gs);
+  if (K % gs) return fail(FLEXQ_ERR_UNSUPPORTED, "K=%d is not a multiple of group_size %d", K, gs);
+  if (N > (1 << 30) || K > (1 << 24)) return fail(FLEXQ_ERR_UNSUPPORTED, "N=%d K=%d too large", N, K);
+  return FLEXQ_OK;
+}
+
+int check_dtype(int dtype) {
+  if (dtype != FLEXQ_DTYPE_FP16 && dtype != FLEXQ_DTYPE_BF16)
+    return fail(FLEXQ_ERR_INVALID_ARG, "dtype=%d is not FLEXQ_DTYPE_FP16 or FLEXQ_DTYPE_BF16", dtype);
+  return FLEXQ_OK;
+}
+
+size_t w4_packed_bytes(int N, int K) {
+  return static_cast<size_t>(flexq::w4_row_tiles(N)) * flexq::w4_col_tiles(K) * flexq::kW4TileBytes;
+}
+
+// ----------------------------------------------------------- linear layers --
+struct GemvPlan {
+  int nt;       // 8-token tiles per CTA
+  int s;        // 16-row strips per CTA
+  int ks;       // CTAs of a cluster that share the columns
+};
+
+constexpr int kGemvStrips = 2;
+
+// Token tiles follow M.  The columns are split over a cluster while the CTAs
+// are fewer than two per SM and every warp keeps at least two column tiles.
+GemvPlan gemv_plan(int M, long long blocks, int kbs, int sms) {
+  GemvPlan p;
+  p.nt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
+  p.s = kGemvStrips;
+  const long long ctas = blocks * ((M + 8 * p.nt - 1) / (8 * p.nt));
+  p.ks = 1;
+  while (p.ks < 8 && ctas * p.ks < 2LL * sms && kbs >= 2 * p.ks * flexq::kGemvWarps) p.ks *= 2;
+  return p;
+}
+
+template <typename T, int NT, int WPG>
+cudaError_t launch_gemv(const flexq::W4Layers& L, const flexq::GemvArgs& a, dim3 grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(flexq::kGemvThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = grid.z;
+  cfg.attrs = attr;
+  cfg.numAttrs = grid.z > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, NT, kGemvStrips, WPG>, L, a);
+}
+
+template <typename T, int NT>
+cudaError_t launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::GemvArgs& a, dim3 grid,
+                           cudaStream_t stream) {
+  return gs == 32   ? launch_gemv<T, NT, 1>(L, a, grid, stream)
+         : gs == 64 ? launch_gemv<T, NT, 2>(L, a, grid, stream)
+                    : launch_gemv<T, NT, 4>(L, a, grid, stream);
+}
+
+template <typename T>
+cudaError_t launch_gemv_nt(int nt, int gs, const flexq::W4Layers& L, const flexq::GemvArgs& a,
+                           dim3 grid, cudaStream_t stream) {
+  return nt == 1   ? launch_gemv_gs<T, 1>(gs, L, a, grid, stream)
+         : nt == 2 ? launch_gemv_gs<T, 2>(gs, L, a, grid, stream)
+                   : launch_gemv_gs<T, 4>(gs, L, a, grid, stream);
+}
+
+int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long ldx, int n_layers,
+                     const flexq_layer4_t* layers, void* stream) {
+  if (n_layers < 1 || n_layers > flexq::kW4MaxLayers)
+    return fail(FLEXQ_ERR_INVALID_ARG, "n_layers=%d is not in 1..%d", n_layers, flexq::kW4MaxLayers);
+  if (!layers) return fail(FLEXQ_ERR_INVALID_ARG, "layers is NULL");
+  if (M < 0) return fail(FLEXQ_ERR_INVALID_ARG, "M=%d is negative", M);
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  for (int l = 0; l < n_layers; ++l)
+    if ((rc = check_w4_shape(layers[l].N, K, gs))) return rc;
+  if (M == 0) return ok();
+  const void* xp[] = {X};
+  const char* xn[] = {"X"};
+  if ((rc = check_ptrs(1, xp, xn))) return rc;
+  if (ldx < K) return fail(FLEXQ_ERR_INVALID_ARG, "ldx=%lld is below K=%d", ldx, K);
+  if (ldx % 8) return fail(FLEXQ_ERR_MISALIGNED, "ldx=%lld is not a multiple of 8 elements", ldx);
+  for (int l = 0; l < n_layers; ++l) {
+    const void* ptrs[] = {layers[l].Wq_packed, layers[l].W_scales};
+    const char* names[] = {"Wq_packed", "W_scales"};
+    if ((rc = check_ptrs(2, ptrs, names))) return rc;
+    if (!layers[l].Y) return fail(FLEXQ_ERR_INVALID_ARG, "Y is NULL");
+    if (reinterpret_cast<uintptr_t>(layers[l].Y) & 1u)
+      return fail(FLEXQ_ERR_MISALIGNED, "Y is not 2-byte aligned");
+    if (layers[l].ldy < layers[l].N)
+      return fail(FLEXQ_ERR_INVALID_ARG, "ldy=%lld is below N=%d", layers[l].ldy, layers[l].N);
+  }
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+
+  flexq::W4Layers L = {};
+  long long blocks = 0;
+  L.n = n_layers;
+  for (int l = 0; l < n_layers; ++l) {
+    L.wp[l] = static_cast<const uint4*>(layers[l].Wq_packed);
+    L.ws[l] = static_cast<const __half*>(layers[l].W_scales);
+    L.y[l] = layers[l].Y;
+    L.ldy[l] = layers[l].ldy;
+    L.N[l] = layers[l].N;
+    L.block0[l] = static_cast<int>(blocks);
+    blocks += (flexq::w4_row_tiles(layers[l].N) + kGemvStrips - 1) / kGemvStrips;
+  }
+  L.block0[n_layers] = static_cast<int>(blocks);
+  flexq::GemvArgs a = {};
+  a.x = X;
+  a.ldx = ldx;
+  a.M = M;
+  a.K = K;
+  a.G = K / gs;
+  a.kbs = flexq::w4_col_tiles(K);
+  a.gs_shift = log2_gs(gs);
+  const GemvPlan p = gemv_plan(M, blocks, a.kbs, st->sms);
+  const int tiles = (M + 8 * p.nt - 1) / (8 * p.nt);
+  // a grid's y extent ends at 65535: more tokens take several launches
+  for (int t0 = 0; t0 < tiles; t0 += 65535) {
+    const int n = std::min(65535, tiles - t0);
+    flexq::GemvArgs at = a;
+    flexq::W4Layers Lt = L;
+    const long long m0 = static_cast<long long>(t0) * 8 * p.nt;
+    at.x = static_cast<const char*>(X) + 2 * m0 * ldx;
+    at.M = static_cast<int>(M - m0);
+    for (int l = 0; l < n_layers; ++l) Lt.y[l] = static_cast<char*>(L.y[l]) + 2 * m0 * L.ldy[l];
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n), static_cast<unsigned>(p.ks));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == FLEXQ_DTYPE_FP16
+                              ? launch_gemv_nt<__half>(p.nt, gs, Lt, at, grid, s)
+                              : launch_gemv_nt<__nv_bfloat16>(p.nt, gs, Lt, at, grid, s);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
+  }
+  return ok();
+}
+
+// ------------------------------------------------------------------ tables --
+int check_table(long long T, int V, int K, int gs, int bits, int dtype, int id_bytes) {
+  if (bits != 4 && bits != 6) return fail(FLEXQ_ERR_INVALID_ARG, "weight_bits=%d is not 4 or 6", bits);
+  if (T < 0) return fail(FLEXQ_ERR_INVALID_ARG, "T=%lld is negative", T);
+  if (T > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "T=%lld too large", T);
+  if (id_bytes != 4 && id_bytes != 8) return fail(FLEXQ_ERR_INVALID_ARG, "id_bytes=%d is not 4 or 8", id_bytes);
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  return bits == 4 ? check_w4_shape(V, K, gs) : check_gemm_shape(0, V, K, gs);
+}
+
+flexq::Table make_table(const void* Wq, const void* Ws, int V, int K, int gs) {
+  flexq::Table t;
+  t.packed = static_cast<const uint8_t*>(Wq);
+  t.scales = static_cast<const __half*>(Ws);
+  t.V = V;
+  t.K = K;
+  t.G = K / gs;
+  t.kbs = flexq::w4_col_tiles(K);
+  t.gs_shift = log2_gs(gs);
+  return t;
+}
+
+template <typename T>
+void launch_embed(int bits, const flexq::Table& tb, const void* ids, int id_bytes, long long units,
+                  float scale, void* out, unsigned grid, cudaStream_t s) {
+  if (bits == 4)
+    flexq::embed_kernel<T, 4><<<grid, 256, 0, s>>>(tb, ids, id_bytes, units, scale, static_cast<T*>(out));
+  else
+    flexq::embed_kernel<T, 6><<<grid, 256, 0, s>>>(tb, ids, id_bytes, units, scale, static_cast<T*>(out));
+}
+
+// Sorted tokens per CTA: two CTAs per SM and column block where there are
+// that many tokens, between 4 (a tile's overhead) and kSumMaxTile.
+int sum_tile(long long T, int K) {
+  const long long cols = (K + flexq::kSumCols - 1) / flexq::kSumCols;
+  const long long tile = T * cols / (2 * 148 * 2);
+  return static_cast<int>(std::max<long long>(4, std::min<long long>(flexq::kSumMaxTile, tile)));
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t backward_workspace(long long T, int K) {
+  if (T <= 0) return 0;
+  const long long tiles = (T + sum_tile(T, K) - 1) / sum_tile(T, K);
+  return 2 * align256(static_cast<size_t>(T) * sizeof(uint2)) +
+         static_cast<size_t>(tiles) * 2 * K * sizeof(float);
+}
+
+template <typename T, typename TO, int BITS>
+void launch_sums(const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.T + static_cast<long long>(a.tile) - 1) / a.tile),
+                  static_cast<unsigned>((tb.K + flexq::kSumCols - 1) / flexq::kSumCols));
+  flexq::embed_sum_kernel<T, TO, BITS><<<grid, flexq::kSumThreads, 0, s>>>(tb, a);
+  if (grid.x > 1) flexq::embed_join_kernel<T, TO, BITS><<<grid, flexq::kSumThreads, 0, s>>>(tb, a);
+}
+
+template <typename T, typename TO>
+void launch_sums_bits(int bits, const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
+  if (bits == 4) launch_sums<T, TO, 4>(tb, a, s);
+  else launch_sums<T, TO, 6>(tb, a, s);
+}
+
+}  // namespace
+
+// ===================================================================== ABI ==
+extern "C" {
+
+size_t flexq_weight4_packed_bytes(int N, int K, int group_size) {
+  if (N <= 0 || K <= 0 || !valid_gs(group_size) || K % group_size || N > (1 << 30) || K > (1 << 24)) return 0;
+  return w4_packed_bytes(N, K);
+}
+
+int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, void* Wq_packed,
+                           void* W_scales_fp16, void* stream) {
+  int rc = check_w4_shape(N, K, group_size);
+  if (rc) return rc;
+  const void* ptrs[] = {W_fp16, Wq_packed, W_scales_fp16};
+  const char* names[] = {"W_fp16", "Wq_packed", "W_scales"};
+  if ((rc = check_ptrs(3, ptrs, names))) return rc;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const __half* w = static_cast<const __half*>(W_fp16);
+  __half* scales = static_cast<__half*>(W_scales_fp16);
+  const long long groups = static_cast<long long>(N) * (K / group_size);
+  const long long words = static_cast<long long>(w4_packed_bytes(N, K) / 4);
+  if ((groups + 7) / 8 > INT32_MAX || (words + 255) / 256 > INT32_MAX)
+    return fail(FLEXQ_ERR_UNSUPPORTED, "N=%d K=%d too large", N, K);
+  flexq::w4_scale_kernel<<<static_cast<unsigned>((groups + 7) / 8), 256, 0, s>>>(w, scales, groups, group_size);
+  flexq::w4_pack_kernel<<<static_cast<unsigned>((words + 255) / 256), 256, 0, s>>>(
+      w, scales, static_cast<uint32_t*>(Wq_packed), N, K, flexq::w4_col_tiles(K), group_size, words);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit quantizer launch");
+  return ok();
+}
+
+int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,
+                    const void* Wq_packed, const void* W_scales, void* Y, long long ldy, void* stream) {
+  const flexq_layer4_t layer = {N, Wq_packed, W_scales, Y, ldy};
+  return linear_w4_common(M, K, group_size, dtype, X, ldx, 1, &layer, stream);
+}
+
+int flexq_linear_w4_group(int M, int K, int group_size, int dtype, const void* X, long long ldx,
+                          int n_layers, const flexq_layer4_t* layers, void* stream) {
+  return linear_w4_common(M, K, group_size, dtype, X, ldx, n_layers, layers, stream);
+}
+
+int flexq_embedding(long long T, int V, int K, int group_size, int weight_bits, int dtype,
+                    const void* ids, int id_bytes, const void* Wq_packed, const void* W_scales,
+                    float scale, void* out, void* stream) {
+  int rc = check_table(T, V, K, group_size, weight_bits, dtype, id_bytes);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  const void* ptrs[] = {Wq_packed, W_scales, out};
+  const char* names[] = {"Wq_packed", "W_scales", "out"};
+  if ((rc = check_ptrs(3, ptrs, names))) return rc;
+  if (!ids) return fail(FLEXQ_ERR_INVALID_ARG, "ids is NULL");
+  if (reinterpret_cast<uintptr_t>(ids) % static_cast<unsigned>(id_bytes))
+    return fail(FLEXQ_ERR_MISALIGNED, "ids is not %d-byte aligned", id_bytes);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+  const flexq::Table tb = make_table(Wq_packed, W_scales, V, K, group_size);
+  const long long units = T * (K / 8);
+  const unsigned grid = static_cast<unsigned>(std::min<long long>((units + 255) / 256, 32LL * st->sms));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == FLEXQ_DTYPE_FP16)
+    launch_embed<__half>(weight_bits, tb, ids, id_bytes, units, scale, out, grid, s);
+  else
+    launch_embed<__nv_bfloat16>(weight_bits, tb, ids, id_bytes, units, scale, out, grid, s);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "embedding launch");
+  return ok();
+}
+
+size_t flexq_embedding_backward_workspace_bytes(long long T, int K) {
+  if (T <= 0 || T > INT32_MAX || K <= 0 || K > (1 << 24)) return 0;
+  return backward_workspace(T, K);
+}
+
+int flexq_embedding_backward(long long T, int V, int K, int group_size, int weight_bits, int dtype,
+                             const void* ids, int id_bytes, const void* dY, const void* Wq_packed,
+                             float scale, int table_dtype, void* d_table, float* d_scales,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_table(T, V, K, group_size, weight_bits, dtype, id_bytes);
+  if (rc) return rc;
+  if (!d_table && !d_scales) return fail(FLEXQ_ERR_INVALID_ARG, "d_table and d_scales are both NULL");
+  if (d_table && table_dtype != dtype && table_dtype != FLEXQ_DTYPE_FP32)
+    return fail(FLEXQ_ERR_INVALID_ARG, "table_dtype=%d is neither dY's type nor FLEXQ_DTYPE_FP32", table_dtype);
+  if (!aligned16(d_table) || !aligned16(d_scales))
+    return fail(FLEXQ_ERR_MISALIGNED, "d_table or d_scales is not 16-byte aligned");
+  const size_t need = backward_workspace(T, K);
+  if (T > 0) {
+    const void* ptrs[] = {dY, workspace};
+    const char* names[] = {"dY", "workspace"};
+    if ((rc = check_ptrs(2, ptrs, names))) return rc;
+    if (!ids) return fail(FLEXQ_ERR_INVALID_ARG, "ids is NULL");
+    if (reinterpret_cast<uintptr_t>(ids) % static_cast<unsigned>(id_bytes))
+      return fail(FLEXQ_ERR_MISALIGNED, "ids is not %d-byte aligned", id_bytes);
+    if (workspace_bytes < need)
+      return fail(FLEXQ_ERR_INVALID_ARG, "workspace of %zu bytes, the call needs %zu", workspace_bytes, need);
+  }
+  if (d_scales) {
+    const void* ptrs[] = {Wq_packed};
+    const char* names[] = {"Wq_packed"};
+    if ((rc = check_ptrs(1, ptrs, names))) return rc;
+  }
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+
+  const flexq::Table tb = make_table(Wq_packed, nullptr, V, K, group_size);
+  const size_t item_bytes = align256(static_cast<size_t>(T) * sizeof(uint2));
+  char* ws = static_cast<char*>(workspace);
+  flexq::SortArgs so = {};
+  so.ids = ids;
+  so.id_bytes = id_bytes;
+  so.T = static_cast<int>(T);
+  so.V = V;
+  for (so.passes = 1; so.passes < 4 && (static_cast<long long>(V) >> (8 * so.passes)); ++so.passes) {}
+  so.buf[0] = reinterpret_cast<uint2*>(ws);
+  so.buf[1] = reinterpret_cast<uint2*>(ws + (T > 0 ? item_bytes : 0));
+  const size_t table_bytes =
+      d_table ? static_cast<size_t>(V) * K * (table_dtype == FLEXQ_DTYPE_FP32 ? 4 : 2) : 0;
+  const size_t scale_elems = d_scales ? static_cast<size_t>(V) * (K / group_size) : 0;
+  so.fill[0] = static_cast<uint4*>(d_table);
+  so.fill[1] = reinterpret_cast<uint4*>(d_scales);
+  so.fill_n[0] = static_cast<long long>(table_bytes / 16);
+  so.fill_n[1] = static_cast<long long>(scale_elems / 4);
+  so.tail = d_scales + scale_elems / 4 * 4;
+  so.tail_n = static_cast<int>(scale_elems % 4);
+  so.clusters_size = T > 1024 ? 8 : 1;
+  const long long pieces = so.fill_n[0] + so.fill_n[1];
+  const long long fillers = std::max<long long>(1, std::min<long long>(2LL * st->sms, (pieces + 4095) / 4096));
+  const int C = so.clusters_size;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(C + (fillers + C - 1) / C * C));
+  cfg.blockDim = dim3(flexq::kSortThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, flexq::embed_sort_kernel, so);
+  if (e != cudaSuccess) return cuda_fail(e, "token sort launch");
+  if (T == 0) return ok();
+
+  flexq::SumArgs a = {};
+  a.sorted = so.buf[(so.passes - 1) & 1];
+  a.dy = dY;
+  a.T = so.T;
+  a.tile = sum_tile(T, K);
+  a.scale = scale;
+  a.partial = reinterpret_cast<float*>(ws + 2 * item_bytes);
+  a.table = d_table;
+  a.scales = d_scales;
+  const bool wide = d_table && table_dtype == FLEXQ_DTYPE_FP32;
+  if (dtype == FLEXQ_DTYPE_FP16) {
+    if (wide) launch_sums_bits<__half, float>(weight_bits, tb, a, cfg.stream);
+    else launch_sums_bits<__half, __half>(weight_bits, tb, a, cfg.stream);
+  } else {
+    if (wide) launch_sums_bits<__nv_bfloat16, float>(weight_bits, tb, a, cfg.stream);
+    else launch_sums_bits<__nv_bfloat16, __nv_bfloat16>(weight_bits, tb, a, cfg.stream);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "embedding gradient launch");
+  return ok();
+}
+
+}  // extern "C"

@@ -33,6 +33,13 @@ class Layer(ctypes.Structure):
                 ("W_scales", ctypes.c_void_p), ("Y_fp16", ctypes.c_void_p)]
 
 
+class Layer4(ctypes.Structure):
+    """flexq_layer4_t: one layer of a grouped 4-bit call."""
+    _fields_ = [("N", ctypes.c_int), ("Wq_packed", ctypes.c_void_p),
+                ("W_scales", ctypes.c_void_p), ("Y", ctypes.c_void_p),
+                ("ldy", ctypes.c_longlong)]
+
+
 class FlexQError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(message)
@@ -49,6 +56,7 @@ def lib():
                 "`python -m bit_group_quantized_flexq_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         c_int, c_void_p, c_size_t = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+        c_ll = ctypes.c_longlong
         sig = {
             "flexq_status_string": (ctypes.c_char_p, [c_int]),
             "flexq_last_error_message": (ctypes.c_char_p, []),
@@ -107,6 +115,19 @@ def lib():
             "flexq_group_plan": (c_int, [c_int, c_int, c_int, c_int, ctypes.POINTER(c_int),
                                          ctypes.POINTER(c_int), ctypes.POINTER(c_int),
                                          ctypes.POINTER(c_int), ctypes.POINTER(c_int)]),
+            "flexq_weight4_packed_bytes": (c_size_t, [c_int, c_int, c_int]),
+            "flexq_quantize_weight4": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p,
+                                               c_void_p, c_void_p]),
+            "flexq_linear_w4": (c_int, [c_int, c_int, c_int, c_int, c_int, c_void_p, c_ll,
+                                        c_void_p, c_void_p, c_void_p, c_ll, c_void_p]),
+            "flexq_linear_w4_group": (c_int, [c_int, c_int, c_int, c_int, c_void_p, c_ll, c_int,
+                                              ctypes.POINTER(Layer4), c_void_p]),
+            "flexq_embedding": (c_int, [c_ll, c_int, c_int, c_int, c_int, c_int, c_void_p, c_int,
+                                        c_void_p, c_void_p, ctypes.c_float, c_void_p, c_void_p]),
+            "flexq_embedding_backward_workspace_bytes": (c_size_t, [c_ll, c_int]),
+            "flexq_embedding_backward": (c_int, [c_ll, c_int, c_int, c_int, c_int, c_int, c_void_p,
+                                                 c_int, c_void_p, c_void_p, ctypes.c_float, c_int,
+                                                 c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -470,3 +491,216 @@ def linear_group(x, weights, group_size, act_bits=6, outs=None, workspace_buf=No
     _check(lib().flexq_linear_group(M, K, group_size, act_bits, _ptr(x), len(weights), arr, wsp,
                                     wsn, _stream(x)))
     return ys
+
+
+# ------------------------------------------- 4-bit layers and packed tables --
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _need_rows(t, name, dtype, shape):
+    """A matrix whose rows are contiguous but may lie further apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+
+
+def _row_stride(t):
+    """Elements between rows (a single row has no stride of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _same_device(x, *others):
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"tensors on {x.device} and {t.device}: all must share one device")
+
+
+def _activation_dtype(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return t.dtype
+
+
+def weight4_packed_bytes(N, K, group_size):
+    return int(lib().flexq_weight4_packed_bytes(N, K, group_size))
+
+
+def quantize_weight4(w, group_size, out=None):
+    """FP16 W [N, K] -> (packed 4-bit codes, uint8 [weight4_packed_bytes(N, K,
+    gs)], FP16 scales [N, K/gs]).  Any N; K a multiple of the group size."""
+    _need(w, "w", torch.float16)
+    if w.dim() != 2:
+        raise ValueError(f"w must be [N, K], got {tuple(w.shape)}")
+    N, K = w.shape
+    nbytes = weight4_packed_bytes(N, K, group_size)
+    if nbytes == 0:
+        raise FlexQError(FLEXQ_ERR_UNSUPPORTED, f"unsupported weight shape {N}x{K}, gs={group_size}")
+    if out is None:
+        out = (torch.empty(nbytes, dtype=torch.uint8, device=w.device),
+               torch.empty(N, K // group_size, dtype=torch.float16, device=w.device))
+    wp, ws = out
+    _need(wp, "packed", torch.uint8, (nbytes,))
+    _need(ws, "scales", torch.float16, (N, K // group_size))
+    _same_device(w, wp, ws)
+    with torch.cuda.device(w.device):
+        _check(lib().flexq_quantize_weight4(N, K, group_size, _ptr(w), _ptr(wp), _ptr(ws),
+                                            _stream(w)))
+    return wp, ws
+
+
+def linear4(x, wp, ws, N, group_size, out=None):
+    """Y [M, N] of a layer with 4-bit weights (quantize_weight4) from FP16 or
+    BF16 activations x [M, K], which are not quantized; Y has x's type.  x and
+    out may be views whose rows lie further apart (x: by a multiple of eight
+    elements)."""
+    return linear4_group(x, [(wp, ws, N)], group_size, outs=[out])[0]
+
+
+def linear4_group(x, weights, group_size, outs=None):
+    """Layers [(wp, ws, N), ...] with 4-bit weights that read the same
+    activations x [M, K] (1..4 layers), in one launch; returns their outputs."""
+    dtype = _activation_dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
+    M, K = x.shape
+    _need_rows(x, "x", dtype, (M, K))
+    if not 1 <= len(weights) <= MAX_GROUP_LAYERS:
+        raise ValueError(f"1..{MAX_GROUP_LAYERS} layers, got {len(weights)}")
+    if outs is not None and len(outs) != len(weights):
+        raise ValueError(f"{len(weights)} layers, {len(outs)} outputs")
+    arr = (Layer4 * len(weights))()
+    ys = []
+    for i, (wp, ws, N) in enumerate(weights):
+        nbytes = weight4_packed_bytes(N, K, group_size)
+        if nbytes == 0:
+            raise FlexQError(FLEXQ_ERR_UNSUPPORTED,
+                             f"unsupported weight shape {N}x{K}, gs={group_size}")
+        _need(wp, "wp", torch.uint8, (nbytes,))
+        _need(ws, "ws", torch.float16, (N, K // group_size))
+        y = outs[i] if outs is not None and outs[i] is not None else \
+            torch.empty(M, N, dtype=dtype, device=x.device)
+        _need_rows(y, "out", dtype, (M, N))
+        _same_device(x, wp, ws, y)
+        arr[i] = Layer4(N, wp.data_ptr(), ws.data_ptr(), y.data_ptr(), max(_row_stride(y), N))
+        ys.append(y)
+    with torch.cuda.device(x.device):
+        _check(lib().flexq_linear_w4_group(M, K, group_size, _DTYPES[dtype], _ptr(x),
+                                           _row_stride(x), len(weights), arr, _stream(x)))
+    return ys
+
+
+def _need_ids(ids):
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    _need(ids, "ids", ids.dtype)
+    return ids.element_size()
+
+
+def _need_table(wp, V, K, group_size, weight_bits):
+    if weight_bits not in (4, 6):
+        raise ValueError(f"weight_bits must be 4 or 6, got {weight_bits!r}")
+    nbytes = (weight4_packed_bytes if weight_bits == 4 else weight_packed_bytes)(V, K, group_size)
+    if nbytes == 0:
+        raise FlexQError(FLEXQ_ERR_UNSUPPORTED,
+                         f"unsupported table shape {V}x{K}, gs={group_size}, {weight_bits} bits")
+    _need(wp, "wp", torch.uint8, (nbytes,))
+
+
+def _scales_shape(V, K, group_size, weight_bits):
+    G = K // group_size
+    return (V, G) if weight_bits == 4 else (G, V)
+
+
+def embedding(ids, wp, ws, V, group_size, scale=1.0, weight_bits=4, dtype=torch.float16, out=None):
+    """Rows of a packed table [V, K]: out[..., :] = scale * dequantized row of
+    each token of ids (int32 or int64, any shape), in FP16 or BF16.  wp, ws:
+    quantize_weight4 (weight_bits 4) or quantize_weight (6, byte-aligned
+    layout).  A token outside [0, V) is padding: its row is zero."""
+    id_bytes = _need_ids(ids)
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+    if weight_bits not in (4, 6):
+        raise ValueError(f"weight_bits must be 4 or 6, got {weight_bits!r}")
+    _need(ws, "ws", torch.float16)
+    if ws.dim() != 2:
+        raise ValueError(f"ws must have two dimensions, got {tuple(ws.shape)}")
+    K = ws.shape[1 if weight_bits == 4 else 0] * group_size
+    _need_table(wp, V, K, group_size, weight_bits)
+    _need(ws, "ws", torch.float16, _scales_shape(V, K, group_size, weight_bits))
+    if out is None:
+        out = torch.empty(*ids.shape, K, dtype=dtype, device=ids.device)
+    _need(out, "out", dtype, (*ids.shape, K))
+    _same_device(ids, wp, ws, out)
+    with torch.cuda.device(ids.device):
+        _check(lib().flexq_embedding(ids.numel(), V, K, group_size, weight_bits, _DTYPES[dtype],
+                                     _ptr(ids), id_bytes, _ptr(wp), _ptr(ws), float(scale),
+                                     _ptr(out), _stream(ids)))
+    return out
+
+
+def embedding_backward_workspace_bytes(T, K):
+    return int(lib().flexq_embedding_backward_workspace_bytes(T, K))
+
+
+def embedding_backward(dy, ids, wp, V, group_size, scale=1.0, weight_bits=4, table_dtype=None,
+                       with_scales=True, out=None, workspace_buf=None):
+    """The gradient of embedding from dy [..., K] (FP16 or BF16): (the rows'
+    gradient [V, K] of table_dtype, dy's type or torch.float32, or None
+    without one; the scales' FP32 gradient, laid out as ws, or None without
+    with_scales).  Rounding to codes is passed through for the rows, codes are
+    constants for the scales.  Both are written whole and do not vary from run
+    to run.
+
+    out:           (rows, scales) to write into;
+    workspace_buf: a uint8 device tensor of at least
+                   embedding_backward_workspace_bytes(tokens, K) bytes that no
+                   other running call uses; by default one of this call's own."""
+    dtype = _activation_dtype(dy, "dy")
+    id_bytes = _need_ids(ids)
+    if dy.dim() < 1:
+        raise ValueError("dy must be [..., K]")
+    T, K = ids.numel(), dy.shape[-1]
+    _need(dy, "dy", dtype, (*ids.shape, K))
+    _need_table(wp, V, K, group_size, weight_bits)
+    if table_dtype not in (None, dtype, torch.float32):
+        raise ValueError(f"table_dtype must be {dtype} or torch.float32, got {table_dtype}")
+    if table_dtype is None and not with_scales:
+        raise ValueError("nothing to compute: neither table_dtype nor with_scales")
+    table, scales = out if out is not None else (None, None)
+    if table_dtype is None:
+        table = None
+    else:
+        if table is None:
+            table = torch.empty(V, K, dtype=table_dtype, device=dy.device)
+        _need(table, "rows", table_dtype, (V, K))
+    shape = _scales_shape(V, K, group_size, weight_bits)
+    if not with_scales:
+        scales = None
+    else:
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.float32, device=dy.device)
+        _need(scales, "scales", torch.float32, shape)
+    if workspace_buf is None:
+        workspace_buf = torch.empty(embedding_backward_workspace_bytes(T, K), dtype=torch.uint8,
+                                    device=dy.device)
+    _need(workspace_buf, "workspace", torch.uint8)
+    _same_device(dy, ids, wp, table, scales, workspace_buf)
+    with torch.cuda.device(dy.device):
+        _check(lib().flexq_embedding_backward(
+            T, V, K, group_size, weight_bits, _DTYPES[dtype], _ptr(ids), id_bytes, _ptr(dy),
+            _ptr(wp), float(scale), _DTYPES[table_dtype] if table is not None else 0,
+            _ptr(table) if table is not None else None,
+            _ptr(scales) if scales is not None else None, _ptr(workspace_buf),
+            workspace_buf.numel(), _stream(dy)))
+    return table, scales

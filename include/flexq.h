@@ -360,6 +360,116 @@ size_t flexq_linear_group_workspace_bytes(int M, int K, int group_size, int n_la
 int flexq_group_plan(int M, int K, int group_size, int n_layers, const int* N, int* tile_tokens,
                      int* k_split, int* ctas, int* launches);
 
+/* ------------------------------------------------------------------------
+ * Weight-only 4-bit layers, and packed tables read by rows
+ * ------------------------------------------------------------------------
+ * Beside the 6-bit weights, whole layers may be kept at 4 bits with the same
+ * group scales and FP16 or BF16 activations that are not quantized, and a
+ * packed matrix of either width may be read by rows (a token embedding that
+ * the output head shares).
+ *   - 4-bit shapes: any N >= 1; K % gs == 0, gs in {32, 64, 128, 256}.
+ *   - None of the calls below keeps a workspace of the library's; those that
+ *     need scratch take it from the caller, per call.
+ */
+#define FLEXQ_DTYPE_FP16 0
+#define FLEXQ_DTYPE_BF16 1
+#define FLEXQ_DTYPE_FP32 2
+
+/*
+ * Size in bytes of the packed 4-bit buffer of an [N, K] layer: N rounded up
+ * to a multiple of 16 times K rounded up to one of 128, half a byte each.
+ * 0 for unsupported shapes.
+ */
+size_t flexq_weight4_packed_bytes(int N, int K, int group_size);
+
+/*
+ * flexq_quantize_weight4 -- offline 4-bit weight quantization and packing, by
+ * the rule of flexq_quantize_weight with Q = 7: s = fp16_rne(absmax / 7),
+ * codes clamp(round_half_even(w / s), -7, 7), all zero where s is 0.
+ *   W_fp16        [N, K] FP16, finite values.
+ *   Wq_packed     out, flexq_weight4_packed_bytes(N, K, gs) bytes.  Tile
+ *                 (nt, kb) holds rows 16 nt .. +15, columns 128 kb .. +127 in
+ *                 1024 bytes at (nt * ceil(K/128) + kb) * 1024; row r is 64
+ *                 bytes at 64 r; 16-byte chunk t of it holds four
+ *                 little-endian words, word w the codes of columns 32 w + 8 t
+ *                 + i (i = 0..7) as u = q + 8 in nibble i/2 + 4 (i%2).  Rows
+ *                 past N and columns past K hold u = 8.
+ *   W_scales_fp16 out, FP16 [N, G] row-major (unlike the group-major scales of
+ *                 the 6-bit form: a row's scales are read together here).
+ */
+int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, void* Wq_packed,
+                           void* W_scales_fp16, void* stream);
+
+/*
+ * flexq_linear_w4 -- Y = X . dequant(Wq)^T with 4-bit weights.
+ *   dtype      FLEXQ_DTYPE_FP16 or FLEXQ_DTYPE_BF16: the type of X and Y.
+ *   X, ldx     [M, K], rows ldx elements apart (ldx >= K, ldx % 8 == 0).
+ *   Y, ldy     out, [M, N], rows ldy >= N elements apart; nothing between the
+ *              rows is written.  Y needs its elements' alignment only.
+ * Y[m,n] = round(sum_g s[n,g] * sum_{k in g} X[m,k] q[n,k]), sums in FP32,
+ * rounded once.  The summation order depends on the shapes alone.
+ */
+int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,
+                    const void* Wq_packed, const void* W_scales, void* Y, long long ldy,
+                    void* stream);
+
+/* One layer of a grouped 4-bit call (see flexq_layer_t). */
+typedef struct flexq_layer4 {
+  int N;
+  const void* Wq_packed;
+  const void* W_scales;
+  void* Y;
+  long long ldy;
+} flexq_layer4_t;
+
+/*
+ * flexq_linear_w4_group -- flexq_linear_w4 for 1 to FLEXQ_MAX_GROUP_LAYERS
+ * layers that read the same X.
+ */
+int flexq_linear_w4_group(int M, int K, int group_size, int dtype, const void* X, long long ldx,
+                          int n_layers, const flexq_layer4_t* layers, void* stream);
+
+/*
+ * flexq_embedding -- rows of a packed table: out[t,:] = scale * q[id_t,:] *
+ * s[id_t, group], each value rounded once to dtype.
+ *   T, ids, id_bytes  T tokens, int32 (id_bytes 4) or int64 (8), aligned to
+ *                     their size.  A token outside [0, V) is padding: its row
+ *                     is zero.
+ *   weight_bits       4: Wq_packed and W_scales of flexq_quantize_weight4;
+ *                     6: of flexq_quantize_weight (FLEXQ_LAYOUT_BYTE_ALIGNED;
+ *                     its shape rules, V % 128 == 0 and K % 256 == 0).
+ *   out               [T, K] of dtype (FP16 or BF16).
+ */
+int flexq_embedding(long long T, int V, int K, int group_size, int weight_bits, int dtype,
+                    const void* ids, int id_bytes, const void* Wq_packed, const void* W_scales,
+                    float scale, void* out, void* stream);
+
+/* Device scratch of flexq_embedding_backward (need not be cleared; 0 for
+ * T <= 0). */
+size_t flexq_embedding_backward_workspace_bytes(long long T, int K);
+
+/*
+ * flexq_embedding_backward -- the gradient of flexq_embedding from dY [T, K]
+ * (dtype): with D[v,k] = scale * sum of dY[t,k] over the tokens t of row v,
+ *   d_table   out, [V, K] of table_dtype (dtype or FLEXQ_DTYPE_FP32), or
+ *             NULL: D, the gradient of a latent table whose rounding to codes
+ *             is passed through.
+ *   d_scales  out, FP32, laid out as the table's scales ([V, G] for 4 bits,
+ *             [G, V] for 6), or NULL: sum_{k in g} D[v,k] * q[v,k], the
+ *             gradient of the group scales under fixed codes (Wq_packed is
+ *             only read for it).
+ * Both are written whole; rows without a token, and padding tokens, give
+ * zeros.  Tokens are sorted by row and each row's are added in FP32 in the
+ * order of the tokens, in pieces whose bounds depend on T and K alone: the
+ * result does not vary from run to run.
+ *   workspace  flexq_embedding_backward_workspace_bytes(T, K) bytes, 16-byte
+ *              aligned, used by this call only while it runs.
+ */
+int flexq_embedding_backward(long long T, int V, int K, int group_size, int weight_bits, int dtype,
+                             const void* ids, int id_bytes, const void* dY, const void* Wq_packed,
+                             float scale, int table_dtype, void* d_table, float* d_scales,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * flexq_debug_check_quantizer -- test hook: runs the GPU quantizer's
  * division-free code rule against the IEEE-division rule (FP32 division by

@@ -1,0 +1,188 @@
+"""4-bit weights on the GPU: the quantizer bit for bit against its plain form,
+and the linear layers against 64-bit sums.
+
+Tolerance of an output: half a rounding step of its type, and the FP32 sums'
+error: a product passes through at most 16 additions inside a tensor-core step
+of 16 columns, 8 steps per tile of 128 columns, one addition per tile of its
+warp, 8 warps and 8 cluster ranks, each off by at most 2^-23 (a truncation) of
+the sum of magnitudes.  FP16 results below the normal range are off by half
+of 2^-24."""
+
+import numpy as np
+import pytest
+import torch
+
+from bit_group_quantized_flexq_b200 import flexq, inputs
+from tests.w4_util import dequantize, half_step, pack4, quantize4, to64
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(N, K, seed):
+    return inputs.weights(N, K, seed=seed)
+
+
+def packed(w, gs):
+    wp, ws = flexq.quantize_weight4(w.cuda(), gs)
+    q, s = quantize4(w.numpy(), gs)
+    return wp, ws, dequantize(q, s)
+
+
+def check(y, x, w64, dtype):
+    x64 = to64(x)
+    ref, mags = x64 @ w64.T, np.abs(x64) @ np.abs(w64).T
+    tiles = -(-x64.shape[1] // 128)
+    tol = (half_step(dtype) * np.abs(ref) + (48 + tiles) * 2.0 ** -23 * mags + 2.0 ** -25)
+    bad = np.abs(to64(y) - ref) > tol
+    assert not bad.any(), f"{bad.sum()} of {bad.size}, worst {np.abs(to64(y) - ref).max()}"
+
+
+def _edge_weights():
+    w = weights(16, 256, 5)
+    w[0, :32] = 0                                       # a group of zeros
+    w[1, :32] = 2.0 ** -24                              # its scale underflows to zero
+    w[2, :32] = torch.linspace(-6e-7, 6e-7, 32)         # a subnormal scale
+    w[3, :32] = 7 * torch.tensor([0.5, -0.5, 1.5, 1, 2.5 / 7, -3.5 / 7, 7, -7] * 4)   # ties
+    w[4, 32:64] = 65504                                 # the largest scale
+    return w
+
+
+@pytest.mark.parametrize("N, K, gs", [(1, 32, 32), (16, 128, 128), (19, 288, 32), (33, 320, 64),
+                                      (100, 512, 256), (257, 1024, 128)])
+def test_quantizer_matches_its_plain_form(N, K, gs):
+    w = weights(N, K, N + K)
+    wp, ws = flexq.quantize_weight4(w.cuda(), gs)
+    q, s = quantize4(w.numpy(), gs)
+    assert np.array_equal(ws.cpu().numpy().view(np.uint16), s.view(np.uint16))
+    assert np.array_equal(wp.cpu().numpy(), pack4(q))
+
+
+def test_quantizer_edge_values():
+    w = _edge_weights()
+    wp, ws = flexq.quantize_weight4(w.cuda(), 32)
+    q, s = quantize4(w.numpy(), 32)
+    assert np.array_equal(ws.cpu().numpy().view(np.uint16), s.view(np.uint16))
+    assert np.array_equal(wp.cpu().numpy(), pack4(q))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("M, N, K, gs", [
+    (1, 1, 32, 32), (1, 100, 160, 32), (2, 16, 128, 128), (3, 257, 288, 32), (5, 33, 320, 64),
+    (7, 48, 192, 64), (8, 1000, 1024, 128), (9, 65, 512, 256), (16, 31, 4096, 128),
+    (17, 129, 768, 256), (31, 40, 2080, 32), (33, 77, 1088, 64), (64, 130, 1024, 256),
+    (70, 129, 640, 128), (130, 300, 1024, 64), (300, 515, 2304, 256), (1, 4096, 4096, 128)])
+def test_linear_against_64_bits(M, N, K, gs, dtype):
+    wp, ws, w64 = packed(weights(N, K, 3 * N + K), gs)
+    x = inputs.activations(M, K, seed=M).to(dtype)
+    y = flexq.linear4(x.cuda(), wp, ws, N, gs)
+    assert y.dtype == dtype and y.shape == (M, N)
+    check(y, x, w64, dtype)
+
+
+@pytest.mark.parametrize("M", [1, 12, 200])
+def test_every_code_is_multiplied_exactly(M):
+    # codes -8 .. 7 in every place of a word, scales that are powers of two and
+    # activations of -2 .. 2: every sum is an integer multiple that FP32 holds
+    N, K, gs = 64, 512, 64
+    rng = np.random.default_rng(M)
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    s = (2.0 ** rng.integers(-3, 1, (N, K // gs))).astype(np.float16)
+    x = torch.from_numpy(rng.integers(-2, 3, (M, K)).astype(np.float16))
+    y = flexq.linear4(x.cuda(), torch.from_numpy(pack4(q).copy()).cuda(),
+                      torch.from_numpy(s).cuda(), N, gs)
+    ref = (x.double().numpy() @ dequantize(q, s).T).astype(np.float16)
+    assert np.array_equal(y.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("M", [1, 6, 40, 150])
+def test_grouped_layers(M):
+    K, gs = 1024, 128
+    Ns = [500, 16, 77, 1]
+    layers = [packed(weights(n, K, n), gs) for n in Ns]
+    x = inputs.activations(M, K, seed=2)
+    ys = flexq.linear4_group(x.cuda(), [(wp, ws, n) for (wp, ws, _), n in zip(layers, Ns)], gs)
+    for y, (_, _, w64) in zip(ys, layers):
+        check(y, x, w64, torch.float16)
+
+
+@pytest.mark.parametrize("M", [3, 20, 140])
+def test_rows_of_wider_matrices(M):
+    # x and out are column slices; what lies beside them is neither read into
+    # the sums nor written
+    N, K, gs = 50, 288, 32
+    wp, ws, w64 = packed(weights(N, K, 9), gs)
+    wide = torch.full((M, K + 64), float("nan"), dtype=torch.float16)
+    x = inputs.activations(M, K, seed=4)
+    wide[:, 32:32 + K] = x
+    out = torch.full((M, N + 9), 7.0, dtype=torch.float16, device="cuda")
+    y = flexq.linear4(wide.cuda()[:, 32:32 + K], wp, ws, N, gs, out=out[:, 4:4 + N])
+    check(y, x, w64, torch.float16)
+    assert (out[:, :4] == 7).all() and (out[:, 4 + N:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [9, 100])
+def test_special_values_stay_in_their_token(M):
+    N, K, gs = 40, 512, 128
+    wp, ws, w64 = packed(weights(N, K, 11), gs)
+    x = inputs.activations(M, K, seed=6)
+    bad = x.clone()
+    bad[2, 5], bad[4, 100] = float("nan"), float("inf")
+    y = flexq.linear4(bad.cuda(), wp, ws, N, gs)
+    assert torch.isnan(y[2]).all()
+    assert not torch.isfinite(y[4]).all()
+    keep = [m for m in range(M) if m not in (2, 4)]
+    check(y[keep], x[keep], w64, torch.float16)
+
+
+def test_no_tokens():
+    wp, ws, _ = packed(weights(16, 128, 1), 128)
+    y = flexq.linear4(torch.empty(0, 128, dtype=torch.float16, device="cuda"), wp, ws, 16, 128)
+    assert y.shape == (0, 16)
+
+
+@pytest.mark.parametrize("M", [1, 24, 160])
+def test_repeats_captured_and_on_another_stream(M):
+    N, K, gs = 300, 2048, 128
+    wp, ws, w64 = packed(weights(N, K, 8), gs)
+    x = inputs.activations(M, K, seed=1).cuda()
+    first = flexq.linear4(x, wp, ws, N, gs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = flexq.linear4(x, wp, ws, N, gs)
+        out = torch.empty_like(first)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        flexq.linear4(x, wp, ws, N, gs, out=out)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first, second) and torch.equal(first, out)
+    x2 = inputs.activations(M, K, seed=77)
+    x.copy_(x2)
+    graph.replay()
+    check(out, x2, w64, torch.float16)
+
+
+def test_refusals_on_the_gpu():
+    wp, ws, _ = packed(weights(16, 256, 1), 128)
+    x = torch.zeros(4, 256, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        flexq.linear4(x, wp, ws, 17 + 16, 128)
+    with pytest.raises(ValueError, match="shape"):
+        flexq.linear4(x, wp, ws.t().contiguous(), 16, 128)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        flexq.linear4(torch.zeros(256, 4, dtype=torch.float16, device="cuda").t(), wp, ws, 16, 128)
+    with pytest.raises(flexq.FlexQError, match="multiple of 8"):
+        flexq.linear4(torch.zeros(4, 260, dtype=torch.float16, device="cuda")[:, :256], wp, ws, 16, 128)
+    with pytest.raises(flexq.FlexQError, match="16-byte aligned"):
+        flexq.linear4(torch.zeros(4, 264, dtype=torch.float16, device="cuda")[:, 4:260], wp, ws, 16, 128)
+    with pytest.raises(flexq.FlexQError, match="below"):
+        flexq.linear4(x[:1].expand(4, 256), wp, ws, 16, 128)
+    with pytest.raises(ValueError, match="out must be"):
+        flexq.linear4(x, wp, ws, 16, 128, out=torch.zeros(4, 16, device="cuda"))
+    with pytest.raises(flexq.FlexQError, match="unsupported"):
+        flexq.linear4(x[:, :160], wp, ws, 16, 128)
+    with pytest.raises(ValueError, match="layers"):
+        flexq.linear4_group(x, [(wp, ws, 16)] * 5, 128)

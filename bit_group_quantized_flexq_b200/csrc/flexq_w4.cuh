@@ -12,6 +12,7 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
+#include "flexq_gemm.cuh"
 #include "flexq_ptx.cuh"
 #include "flexq_quant.cuh"
 
@@ -22,15 +23,15 @@ namespace flexq {
 // 0).  Tile (nt, kb) = rows 16 nt .. +15, columns 128 kb .. +127 is 1024
 // contiguous bytes at (nt * kbs + kb) * 1024; row r of it is 64 bytes at
 // 64 r; its 16-byte chunk t holds four little-endian words, and word w the
-// eight codes of columns 32 w + 8 t .. +7 as u = q + 8, column i in nibble
-// i / 2 + 4 * (i % 2).
+// eight codes of columns 32 w + 8 t .. +7 as u = q + 8: columns 0, 2, 4 and 6
+// in nibbles 0, 2, 1 and 3, the odd column behind each four nibbles higher.
 //
 // Why: a warp's 16-byte loads of a tile cover 512 contiguous bytes, lane
 // (4 r + t) holding row r's chunk t, which is the register layout of an
 // m16n8k16 MMA's A operand up to the order of k; that order is chosen so that
 // the lane's activations for one word are 16 contiguous bytes too.  The
 // nibble order puts consecutive columns into the two halves of a register
-// with one mask.  A row's 128 codes stay within 64 aligned bytes (two DRAM
+// with one mask, and columns 0 .. 3 and 4 .. 7 into the same bits of them.  A row's 128 codes stay within 64 aligned bytes (two DRAM
 // sectors), so that rows can also be looked up alone.
 constexpr int kW4TileRows = 16;
 constexpr int kW4TileCols = 128;
@@ -45,9 +46,12 @@ __device__ __forceinline__ size_t w4_word_offset(int n, int k, int kbs) {
          ((k >> 3) & 3) * 16 + ((k >> 5) & 3) * 4;
 }
 
-// Code i (0..7) of a word.
+// The bit at which code i (0..7) of a word begins, and the code.
+__host__ __device__ constexpr int w4_shift(int i) {
+  return 4 * ((i >> 1 & 1) * 2 + (i >> 2) + 4 * (i & 1));
+}
 __device__ __forceinline__ int w4_code(uint32_t word, int i) {
-  return static_cast<int>((word >> (4 * (i / 2 + 4 * (i & 1)))) & 15u) - 8;
+  return static_cast<int>((word >> w4_shift(i)) & 15u) - 8;
 }
 
 // --------------------------------------------------------------- quantizer --
@@ -83,13 +87,20 @@ __global__ void w4_pack_kernel(const __half* __restrict__ w, const __half* __res
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int q = quant_code_div(__half2float(h[j]), s, 7);
-      word |= static_cast<uint32_t>(q + 8) << (4 * (j / 2 + 4 * (j & 1)));
+      word |= static_cast<uint32_t>(q + 8) << w4_shift(j);
     }
   }
   packed[i] = word;
 }
 
 // ---------------------------------------------------------- element types --
+// (w & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
+}
+
 template <typename T>
 struct Elem;
 
@@ -105,13 +116,15 @@ struct Elem<__half> {
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
   }
+  // d = a . b + c
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-    asm volatile(
+                                             uint32_t b1, const float (&c)[4]) {
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
   }
   // The eight codes of a word as exact FP16 pairs of consecutive columns.  A
   // nibble in the low mantissa bits of 1024 is 1024 + u; four bits further up
@@ -122,16 +135,29 @@ struct Elem<__half> {
     const __half2 off16 = __half2half2(__ushort_as_half(0xD480));    // -72
     const uint32_t v = w >> 8;
     uint32_t b[4];
-    b[0] = (w & 0x000F000Fu) | 0x64006400u;
-    b[1] = (w & 0x00F000F0u) | 0x64006400u;
-    b[2] = (v & 0x000F000Fu) | 0x64006400u;
-    b[3] = (v & 0x00F000F0u) | 0x64006400u;
+    b[0] = and_or(w, 0x000F000Fu, 0x64006400u);
+    b[1] = and_or(w, 0x00F000F0u, 0x64006400u);
+    b[2] = and_or(v, 0x000F000Fu, 0x64006400u);
+    b[3] = and_or(v, 0x00F000F0u, 0x64006400u);
     __half2* h = reinterpret_cast<__half2*>(b);
     __half2* o = reinterpret_cast<__half2*>(p);
     o[0] = __hsub2(h[0], off);
-    o[1] = __hfma2(h[1], sixteenth, off16);
-    o[2] = __hsub2(h[2], off);
+    o[1] = __hsub2(h[2], off);
+    o[2] = __hfma2(h[1], sixteenth, off16);
     o[3] = __hfma2(h[3], sixteenth, off16);
+  }
+  // The same without the subtraction, for a product corrected by the sum of
+  // the activations: u in the lowest mantissa bits of a subnormal (columns
+  // 0 .. 3, u * 2^-24), or four bits up (4 .. 7, 16 u * 2^-24).  Exact.
+  static constexpr float kOffset = 8.0f / 16777216.0f;     // of columns 0 .. 3
+  static constexpr float kHigh = 1.0f / 16.0f;             // columns 4 .. 7 to their unit
+  static constexpr float kUnit = 16777216.0f;
+  static __device__ __forceinline__ void offset_codes(uint32_t w, uint32_t (&p)[4]) {
+    const uint32_t v = w >> 8;
+    p[0] = w & 0x000F000Fu;
+    p[1] = v & 0x000F000Fu;
+    p[2] = w & 0x00F000F0u;
+    p[3] = v & 0x00F000F0u;
   }
 };
 
@@ -147,13 +173,15 @@ struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
   }
+  // d = a . b + c
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-    asm volatile(
+                                             uint32_t b1, const float (&c)[4]) {
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
   }
   // BF16 has 7 mantissa bits: a nibble in the low ones of 128 is 128 + u; the
   // other nibbles are shifted there first.
@@ -161,39 +189,393 @@ struct Elem<__nv_bfloat16> {
     const __nv_bfloat162 off = __bfloat162bfloat162(__ushort_as_bfloat16(0x4308));   // 136
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t b = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      const uint32_t b = and_or(w >> w4_shift(2 * i), 0x000F000Fu, 0x43004300u);
       const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), off);
       p[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
+  }
+  // Without the subtraction: u in the upper four mantissa bits of 16 is
+  // 16 + u = q + 24.  (In a subnormal it would leave the sums no precision.)
+  static constexpr float kOffset = 24.0f;
+  static constexpr float kHigh = 1.0f;
+  static constexpr float kUnit = 1.0f;
+  static __device__ __forceinline__ void offset_codes(uint32_t w, uint32_t (&p)[4]) {
+    p[0] = and_or(w << 3, 0x00780078u, 0x41804180u);
+    p[1] = and_or(w >> 5, 0x00780078u, 0x41804180u);
+    p[2] = and_or(w >> 1, 0x00780078u, 0x41804180u);
+    p[3] = and_or(w >> 9, 0x00780078u, 0x41804180u);
   }
 };
 
 // ---------------------------------------------------- matrix-vector product --
 constexpr int kW4MaxLayers = 4;
-constexpr int kGemvWarps = 8;
-constexpr int kGemvThreads = kGemvWarps * 32;
 
-// The layers of one launch: they read the same activations.
+// The layers of one launch: they read the same activations.  Strips of 16
+// rows are numbered layer after layer.
 struct W4Layers {
   const uint4* wp[kW4MaxLayers];
   const __half* ws[kW4MaxLayers];
   void* y[kW4MaxLayers];
   long long ldy[kW4MaxLayers];
   int N[kW4MaxLayers];
-  int block0[kW4MaxLayers + 1];   // first block (in x) of each layer
+  int strip0[kW4MaxLayers + 1];
   int n;
 };
 
-struct GemvArgs {
+struct W4Args {
   const void* x;
   long long ldx;
   int M, K, G, kbs, gs_shift;     // kbs: tiles of 128 columns; gs = 1 << gs_shift
+  unsigned int* status;           // device status word
+  unsigned long long wait_limit_ns;
 };
+
+// The product for batches of up to 8 tokens streams the weights once, so it is
+// bound by HBM; every SM must keep tens of KB of loads in flight from its
+// first to its last cycle.  A strip's tiles are cut into chunks of four tiles
+// (16 rows x 512 columns, 4 KB, one bulk copy); the chunks of a run of strips
+// are divided evenly among the 32 warps of a cluster of two CTAs (a pair of
+// SMs), wherever strips begin or end: no warp waits for another before the
+// end.  A warp brings a chunk into a buffer of its own while it multiplies the
+// one before in registers; the activations lie in shared memory.  Codes are exact in FP16 and BF16; the tensor core adds a
+// group's products in FP32, and the group's sum times the scale is added in
+// FP32.  What a warp has of a strip that it shares with others goes to shared
+// memory and is added, in the order of the columns, by the warp that holds the
+// strip's first chunk.
+//
+// Taking a code apart has to cost little: at HBM's rate an SM has about 44
+// cycles per tile.  So the tensor core multiplies codes with an offset, u = q
+// + 8 (in units that differ by type), which takes one mask each, and a group's
+// product starts from minus the offset times the sum of its activations,
+// which every CTA forms once while its first weights are on the way.
+constexpr int kGemvWarps = 16;
+constexpr int kGemvThreads = kGemvWarps * 32;
+constexpr int kGemvCluster = 2;
+constexpr int kGemvShares = kGemvWarps * kGemvCluster;
+constexpr int kGemvChunk = 4;                 // tiles
+constexpr int kGemvChunkBytes = kGemvChunk * kW4TileBytes;
+constexpr int kGemvBufferBytes = kGemvWarps * kGemvChunkBytes;
+
+// The scales of a row for a chunk: NS of them, as FP16 bits in pairs.
+template <int NS>
+struct ChunkScales {
+  uint32_t v[(NS + 1) / 2];
+  __device__ __forceinline__ float get(int i) const {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(v[i / 2] >> (16 * (i & 1)))));
+  }
+  // `left` scales from p on belong to the row (none: a row behind the last).
+  // `even`: every chunk is whole and its scales are aligned for wide loads.
+  __device__ __forceinline__ void load(const __half* p, int left, bool even) {
+    if (even && left > 0) {
+      if constexpr (NS == 1) {
+        v[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+      } else if constexpr (NS == 2) {
+        v[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else if constexpr (NS == 4) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        v[0] = u.x;
+        v[1] = u.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NS / 8; ++i) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          v[4 * i] = u.x;
+          v[4 * i + 1] = u.y;
+          v[4 * i + 2] = u.z;
+          v[4 * i + 3] = u.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NS; i += 2) {
+        uint32_t lo = 0, hi = 0;
+        if (i < left) lo = __ldg(reinterpret_cast<const unsigned short*>(p) + i);
+        if (NS > 1 && i + 1 < left) hi = __ldg(reinterpret_cast<const unsigned short*>(p) + i + 1);
+        v[i / 2] = lo | hi << 16;
+      }
+    }
+  }
+};
+
+// acc += one 16 x 128 tile times the activations of eight tokens.  c0, c1:
+// scales of rows g and g + 8; xs: for each group of the chunk, minus the
+// codes' offset times the sum of the activations of tokens 2 t and 2 t + 1;
+// WPG: words (of 32 columns) per group, 8 where a group is two tiles.
+template <typename T, int WPG, int NS>
+__device__ __forceinline__ void gemv_tile(float (&acc)[4], const uint4& w0, const uint4& w1,
+                                          const uint4 (&xv)[4], const ChunkScales<NS>& c0,
+                                          const ChunkScales<NS>& c1, const float* xs, int tile) {
+  float lower[4], upper[4];         // columns 0 .. 3 and 4 .. 7 of the words
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t lo[4], hi[4];
+    Elem<T>::offset_codes(reinterpret_cast<const uint32_t*>(&w0)[j], lo);
+    Elem<T>::offset_codes(reinterpret_cast<const uint32_t*>(&w1)[j], hi);
+    const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
+    const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+    const int i = (tile * 4 + j) / WPG;
+    if (j % WPG == 0) {
+      float2 o = make_float2(0.0f, 0.0f);         // the second tile of a group goes on
+      if (WPG <= 4 || tile % 2 == 0) o = *reinterpret_cast<const float2*>(xs + 8 * i);
+      const float from[4] = {o.x, o.y, o.x, o.y}, zero[4] = {};
+      Elem<T>::mma(lower, a0, xv[j].x, xv[j].y, from);
+      Elem<T>::mma(upper, a1, xv[j].z, xv[j].w, zero);
+    } else {
+      Elem<T>::mma(lower, a0, xv[j].x, xv[j].y, lower);
+      Elem<T>::mma(upper, a1, xv[j].z, xv[j].w, upper);
+    }
+    if ((j + 1) % WPG == 0 || j == 3) {
+      const float f0 = c0.get(i), f1 = c1.get(i);
+      acc[0] = fmaf(fmaf(upper[0], Elem<T>::kHigh, lower[0]), f0, acc[0]);
+      acc[1] = fmaf(fmaf(upper[1], Elem<T>::kHigh, lower[1]), f0, acc[1]);
+      acc[2] = fmaf(fmaf(upper[2], Elem<T>::kHigh, lower[2]), f1, acc[2]);
+      acc[3] = fmaf(fmaf(upper[3], Elem<T>::kHigh, lower[3]), f1, acc[3]);
+    }
+  }
+}
+
+// Bytes of a token's activations in shared memory: whole tiles (zeros behind
+// K), and half a bank line so that tokens' rows start in different banks.
+__host__ __device__ constexpr int gemv_x_stride(int kbs) { return kbs * kW4TileCols * 2 + 64; }
+
+// The sums of activations are kept for every group of the padded columns.
+__host__ __device__ constexpr int gemv_smem(int M, int kbs, int gs_shift) {
+  return kGemvBufferBytes + M * gemv_x_stride(kbs) +
+         (((kbs * kW4TileCols - 1) >> gs_shift) + 1) * 8 * static_cast<int>(sizeof(float));
+}
+
+template <typename T, int WPG>
+__global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_constant__ W4Layers L,
+                                                                 const W4Args a) {
+  constexpr int NS = 4 * kGemvChunk / WPG;        // scales of a row per chunk
+  extern __shared__ __align__(128) uint8_t buffers[];
+  const int kbs = a.kbs, x_stride = gemv_x_stride(kbs);
+  uint8_t* xs_mem = buffers + kGemvBufferBytes;                            // [M][x_stride]
+  float* xsum = reinterpret_cast<float*>(xs_mem + a.M * x_stride);        // [groups][8 tokens]
+  __shared__ uint64_t full[kGemvWarps];
+  __shared__ uint64_t x_full;
+  // [0]: a strip begun by an earlier warp; [1]: one that a later warp ends
+  __shared__ float4 part_of[2][kGemvWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = blockIdx.x % kGemvCluster;
+  const long long cluster = blockIdx.x / kGemvCluster, clusters = gridDim.x / kGemvCluster;
+  const int strips = L.strip0[L.n];
+  const int per_strip = (kbs + kGemvChunk - 1) / kGemvChunk;
+  const int first = static_cast<int>(cluster * strips / clusters);
+  const int units = (static_cast<int>((cluster + 1) * strips / clusters) - first) * per_strip;
+  const int share = rank * kGemvWarps + warp;
+  auto begin_of = [&](int w) { return static_cast<int>(static_cast<long long>(w) * units / kGemvShares); };
+  auto layer_of = [&](int strip) {
+    int l = 0;
+    while (l + 1 < L.n && strip >= L.strip0[l + 1]) ++l;
+    return l;
+  };
+  const int u0 = begin_of(share), u1 = begin_of(share + 1);
+  uint8_t* buffer = buffers + warp * kGemvChunkBytes;
+  const int tail_tiles = kbs - (per_strip - 1) * kGemvChunk;              // of a strip's last chunk
+
+  int c = u0 % per_strip, strip = first + u0 / per_strip;   // of the chunk in hand
+  // the next chunk to request, its place in its strip and in memory
+  int ru = u0, rc = c, rs = strip;
+  const uint4* rp = nullptr;
+  auto stream_at = [&](int strip, int c) {
+    const int l = layer_of(strip);
+    return L.wp[l] + (static_cast<size_t>(strip - L.strip0[l]) * kbs + c * kGemvChunk) * (kW4TileBytes / 16);
+  };
+  auto request = [&]() {
+    if (ru >= u1) return;
+    const bool end = rc + 1 == per_strip;
+    const int tiles = end ? tail_tiles : kGemvChunk;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[warp], tiles * kW4TileBytes);
+      bulk_load(buffer, rp, tiles * kW4TileBytes, &full[warp]);
+    }
+    ++ru;
+    ++rc;
+    rp += tiles * (kW4TileBytes / 16);
+    if (end) {
+      rc = 0;
+      ++rs;
+      if (L.n > 1 && ru < u1) rp = stream_at(rs, 0);        // perhaps another layer's
+    }
+  };
+  if (u0 < u1) rp = stream_at(strip, c);
+  if (lane == 0) {
+    mbar_init(&full[warp], 1);
+    if (warp == 0) mbar_init(&x_full, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  request();
+
+  // where the scales of rows g and g + 8 lie, from the next chunk on
+  const bool even = a.K % (kGemvChunk * kW4TileCols) == 0;
+  const __half *p0 = nullptr, *p1 = nullptr;
+  int left0 = 0, left1 = 0;                       // of the row; none behind the last row
+  auto rows_of = [&](int strip, int c) {
+    const int l = layer_of(strip);
+    const int row = (strip - L.strip0[l]) * 16 + g;
+    p0 = L.ws[l] + static_cast<size_t>(row) * a.G + c * NS;
+    p1 = p0 + static_cast<size_t>(8) * a.G;
+    left0 = row < L.N[l] ? a.G - c * NS : 0;
+    left1 = row + 8 < L.N[l] ? a.G - c * NS : 0;
+  };
+  ChunkScales<NS> c0, c1, n0, n1;
+  if (u0 < u1) {
+    rows_of(strip, c);
+    c0.load(p0, left0, even);
+    c1.load(p1, left1, even);
+  }
+  // activations to shared memory; columns behind K are zeros
+  const int row_bytes = a.K * 2, pad16 = (kbs * kW4TileCols * 2 - row_bytes) / 16;
+  for (int i = threadIdx.x; i < a.M * pad16; i += kGemvThreads)
+    *reinterpret_cast<uint4*>(xs_mem + i / pad16 * x_stride + row_bytes + i % pad16 * 16) = make_uint4(0, 0, 0, 0);
+  grid_launch_dependents();
+  grid_wait_dependencies();         // weights are constants; activations are not
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(&x_full, a.M * row_bytes);
+    for (int m = 0; m < a.M; ++m)
+      bulk_load(xs_mem + m * x_stride, static_cast<const T*>(a.x) + m * a.ldx, row_bytes, &x_full);
+  }
+  __syncthreads();                  // x_full is initialised; the padding is written
+  bool ok = __syncthreads_and(mbar_wait(&x_full, 0, a.wait_limit_ns));
+  if (!ok && threadIdx.x == 0) record_status(a.status, kStatusTimeout, 2);
+
+  // the sums of the activations of each token and group, gs / 8 lanes to a
+  // group; behind K they are zero like the scales there
+  const int padded = kbs * kW4TileCols, vecs = (padded / 8 + 31) / 32 * 32;
+  for (int i = threadIdx.x; i < a.M * vecs; i += kGemvThreads) {
+    const int m = i / vecs, k = (i - m * vecs) * 8;
+    float sum = 0.0f;
+    if (k < padded) {
+      const uint4 v = *reinterpret_cast<const uint4*>(xs_mem + m * x_stride + k * 2);
+      const float2 q0 = Elem<T>::unpack(v.x), q1 = Elem<T>::unpack(v.y);
+      const float2 q2 = Elem<T>::unpack(v.z), q3 = Elem<T>::unpack(v.w);
+      sum = ((q0.x + q0.y) + (q1.x + q1.y)) + ((q2.x + q2.y) + (q3.x + q3.y));
+    }
+#pragma unroll
+    for (int o = 2 * WPG; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (k < padded && lane % (4 * WPG) == 0) xsum[(k >> a.gs_shift) * 8 + m] = -Elem<T>::kOffset * sum;
+  }
+  __syncthreads();
+
+  // a column of the product without a token is computed and dropped
+  const uint8_t* x = xs_mem + min(g, a.M - 1) * x_stride + t * 16;
+  auto store = [&](int strip, const float (&v)[4]) {
+    const int l = layer_of(strip);
+    const int row = (strip - L.strip0[l]) * 16 + g;
+    T* y = static_cast<T*>(L.y[l]) + row;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = 2 * t + (i & 1);
+      if (m < a.M && row + 8 * (i >> 1) < L.N[l])
+        y[m * L.ldy[l] + 8 * (i >> 1)] = Elem<T>::from_float(v[i] * Elem<T>::kUnit);
+    }
+  };
+  float acc[4] = {};
+  bool whole = c == 0;              // the strip's first chunk is this warp's
+  uint32_t parity = 0;
+#pragma unroll 1
+  for (int u = u0; ok && u < u1; ++u, parity ^= 1) {
+    const bool end = c + 1 == per_strip;
+    if (u + 1 < u1) {               // the next chunk's scales
+      if (end) {
+        rows_of(strip + 1, 0);
+      } else {
+        p0 += NS;
+        p1 += NS;
+        left0 -= NS;
+        left1 -= NS;
+      }
+      n0.load(p0, left0, even);
+      n1.load(p1, left1, even);
+    }
+    if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full[warp]), parity))) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[warp], parity, a.wait_limit_ns));
+      if (!ok) {
+        if (lane == 0) record_status(a.status, kStatusTimeout, 2);
+        break;
+      }
+    }
+    const uint4* tile = reinterpret_cast<const uint4*>(buffer) + lane;
+    uint4 w[kGemvChunk][2];
+#pragma unroll
+    for (int i = 0; i < kGemvChunk; ++i) {
+      w[i][0] = tile[i * 64];
+      w[i][1] = tile[i * 64 + 32];
+    }
+    __syncwarp();                   // every lane holds the chunk
+    request();                      // the next one comes while this one is multiplied
+    const uint4* xp = reinterpret_cast<const uint4*>(x + c * (kGemvChunk * kW4TileCols * 2));
+    const float* xs = xsum + c * NS * 8 + 2 * t;
+    auto multiply = [&](int i) {
+      const uint4 xv[4] = {xp[i * 16], xp[i * 16 + 4], xp[i * 16 + 8], xp[i * 16 + 12]};
+      gemv_tile<T, WPG, NS>(acc, w[i][0], w[i][1], xv, c0, c1, xs, i);
+    };
+    if (!end || tail_tiles == kGemvChunk) {
+#pragma unroll
+      for (int i = 0; i < kGemvChunk; ++i) multiply(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGemvChunk; ++i)
+        if (i < tail_tiles) multiply(i);
+    }
+    c0 = n0;
+    c1 = n1;
+    ++c;
+    if (end) {
+      if (whole) store(strip, acc);
+      else part_of[0][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      whole = true;
+      acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+      c = 0;
+      ++strip;
+    }
+  }
+  if (!ok) {                        // let the copies in flight land
+    mbar_wait(&x_full, 0, a.wait_limit_ns);
+    if (ru > u0) mbar_wait(&full[warp], (ru - u0 - 1) & 1, a.wait_limit_ns);
+  }
+  const bool open = u0 < u1 && c > 0;           // the last strip goes on behind this warp
+  if (open) part_of[whole ? 1 : 0][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  cluster_sync_all();
+  if (open && whole) {
+    const int end = (strip - first + 1) * per_strip;
+    constexpr int kBatch = 8;       // loads from the other warps in flight
+    for (int w0 = share + 1; w0 < kGemvShares && begin_of(w0) < end; w0 += kBatch) {
+      float4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int w2 = w0 + i;
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // a warp without chunks has nothing to add
+        if (w2 < kGemvShares && begin_of(w2) < end && begin_of(w2) < begin_of(w2 + 1))
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[i].x), "=f"(v[i].y), "=f"(v[i].z), "=f"(v[i].w)
+                       : "r"(map_to_rank(smem_u32(&part_of[0][w2 % kGemvWarps][lane]), w2 / kGemvWarps))
+                       : "memory");
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        acc[0] += v[i].x;
+        acc[1] += v[i].y;
+        acc[2] += v[i].z;
+        acc[3] += v[i].w;
+      }
+    }
+    store(strip, acc);
+  }
+  cluster_sync_all();               // no CTA leaves while another reads its part
+}
+
+// -------------------------------------------------------- larger batches --
+constexpr int kBatchWarps = 8;
+constexpr int kBatchThreads = kBatchWarps * 32;
 
 // Registers of one step: a 16 x 128 tile per strip and the batch's
 // activations for its columns.
 template <int NT, int S>
-struct GemvStep {
+struct BatchStep {
   uint4 w[S][2];                  // rows g and g + 8 of each strip
   uint4 x[NT][4];                 // per word: eight columns of token g
 };
@@ -205,14 +587,18 @@ struct GemvStep {
 // totals.  The warps' totals are added in shared memory, the cluster's in
 // distributed shared memory, always in the same order.
 template <typename T, int NT, int S, int WPG>
-__global__ void __launch_bounds__(kGemvThreads) w4_gemv_kernel(const __grid_constant__ W4Layers L,
-                                                              const GemvArgs a) {
+__global__ void __launch_bounds__(kBatchThreads) w4_batch_kernel(const __grid_constant__ W4Layers L,
+                                                              const W4Args a) {
   constexpr int kRows = 16 * S, kTok = 8 * NT;
-  __shared__ float red[kGemvWarps][S * NT * 4][32];
+  __shared__ float red[kBatchWarps][S * NT * 4][32];
   __shared__ float tot[kRows * kTok];
-  int l = 0;
-  while (l + 1 < L.n && static_cast<int>(blockIdx.x) >= L.block0[l + 1]) ++l;
-  const int strip0 = (static_cast<int>(blockIdx.x) - L.block0[l]) * S;
+  // the layer that the block's number falls into, S strips to a block
+  int l = 0, block = blockIdx.x;
+  while (l + 1 < L.n && block >= (L.strip0[l + 1] - L.strip0[l] + S - 1) / S) {
+    block -= (L.strip0[l + 1] - L.strip0[l] + S - 1) / S;
+    ++l;
+  }
+  const int strip0 = block * S;
   const int N = L.N[l], strips = w4_row_tiles(N);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int m0 = blockIdx.y * kTok;
@@ -222,7 +608,7 @@ __global__ void __launch_bounds__(kGemvThreads) w4_gemv_kernel(const __grid_cons
   const __half* ws = L.ws[l];
 
   float acc[S][NT][4] = {};
-  auto load = [&](GemvStep<NT, S>& st, int kb) {
+  auto load = [&](BatchStep<NT, S>& st, int kb) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const bool in = strip0 + s < strips;
@@ -243,9 +629,9 @@ __global__ void __launch_bounds__(kGemvThreads) w4_gemv_kernel(const __grid_cons
       }
     }
   };
-  const int stride = kGemvWarps * ks;
-  int kb = rank * kGemvWarps + warp;
-  GemvStep<NT, S> cur, nxt;
+  const int stride = kBatchWarps * ks;
+  int kb = rank * kBatchWarps + warp;
+  BatchStep<NT, S> cur, nxt;
   if (kb < a.kbs) load(cur, kb);
   for (; kb < a.kbs; kb += stride) {
     if (kb + stride < a.kbs) load(nxt, kb + stride);
@@ -264,8 +650,8 @@ __global__ void __launch_bounds__(kGemvThreads) w4_gemv_kernel(const __grid_cons
         const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          Elem<T>::mma(part[nt], a0, cur.x[nt][w].x, cur.x[nt][w].y);
-          Elem<T>::mma(part[nt], a1, cur.x[nt][w].z, cur.x[nt][w].w);
+          Elem<T>::mma(part[nt], a0, cur.x[nt][w].x, cur.x[nt][w].y, part[nt]);
+          Elem<T>::mma(part[nt], a1, cur.x[nt][w].z, cur.x[nt][w].w, part[nt]);
         }
         if ((w + 1) % WPG == 0) {
           const int k = kb * 128 + w * 32;
@@ -295,19 +681,19 @@ __global__ void __launch_bounds__(kGemvThreads) w4_gemv_kernel(const __grid_cons
       for (int i = 0; i < 4; ++i) red[warp][(s * NT + nt) * 4 + i][lane] = acc[s][nt][i];
   __syncthreads();
   // tot[token][row]: value i of lane (g, t) is row g + 8 (i / 2), token 2 t + i % 2
-  for (int o = threadIdx.x; o < kRows * kTok; o += kGemvThreads) {
+  for (int o = threadIdx.x; o < kRows * kTok; o += kBatchThreads) {
     const int row = o % kRows, tok = o / kRows;
     const int s = row >> 4, nt = tok >> 3;
     const int i = ((row >> 3) & 1) * 2 + (tok & 1), ln = (row & 7) * 4 + ((tok & 7) >> 1);
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kGemvWarps; ++w) v += red[w][(s * NT + nt) * 4 + i][ln];
+    for (int w = 0; w < kBatchWarps; ++w) v += red[w][(s * NT + nt) * 4 + i][ln];
     tot[o] = v;
   }
   if (ks > 1) cluster_sync_all(); else __syncthreads();
   // the cluster's CTAs share the outputs; each adds the ranks' totals in order
   T* y = static_cast<T*>(L.y[l]);
-  for (int o = rank * kGemvThreads + threadIdx.x; o < kRows * kTok; o += kGemvThreads * ks) {
+  for (int o = rank * kBatchThreads + threadIdx.x; o < kRows * kTok; o += kBatchThreads * ks) {
     const int row = strip0 * 16 + o % kRows, m = m0 + o / kRows;
     float v = 0.0f;
     if (ks == 1) {

@@ -29,31 +29,75 @@ size_t w4_packed_bytes(int N, int K) {
 }
 
 // ----------------------------------------------------------- linear layers --
-struct GemvPlan {
-  int nt;       // 8-token tiles per CTA
-  int s;        // 16-row strips per CTA
-  int ks;       // CTAs of a cluster that share the columns
-};
+constexpr int kGemvTokens = 8;    // batches of the streaming kernel
+constexpr int kGemvSmem = 208 * 1024;   // its buffers, activations and their sums
+constexpr int kBatchStrips = 2;   // 16-row strips per CTA of the batch kernel
 
-constexpr int kGemvStrips = 2;
+// Lets a kernel use more than 48 KB of shared memory, once per device.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, bool (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_dev_mutex);
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
 
-// Token tiles follow M.  The columns are split over a cluster while the CTAs
-// are fewer than two per SM and every warp keeps at least two column tiles.
-GemvPlan gemv_plan(int M, long long blocks, int kbs, int sms) {
-  GemvPlan p;
-  p.nt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
-  p.s = kGemvStrips;
-  const long long ctas = blocks * ((M + 8 * p.nt - 1) / (8 * p.nt));
-  p.ks = 1;
-  while (p.ks < 8 && ctas * p.ks < 2LL * sms && kbs >= 2 * p.ks * flexq::kGemvWarps) p.ks *= 2;
-  return p;
+template <typename T, int WPG>
+cudaError_t launch_gemv(const flexq::W4Layers& L, const flexq::W4Args& a, int sms, cudaStream_t stream) {
+  static bool ready[kMaxDevices];
+  const cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG>, kGemvSmem, ready);
+  if (e != cudaSuccess) return e;
+  // one cluster per pair of SMs, and none without a strip
+  const int clusters = std::max(1, std::min(L.strip0[L.n], sms / 2));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * flexq::kGemvCluster));
+  cfg.blockDim = dim3(flexq::kGemvThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(flexq::gemv_smem(a.M, a.kbs, a.gs_shift));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = flexq::kGemvCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // the first weights are requested while the previous kernel finishes
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG>, L, a);
+}
+
+template <typename T>
+cudaError_t launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, int sms,
+                           cudaStream_t stream) {
+  return gs == 32    ? launch_gemv<T, 1>(L, a, sms, stream)
+         : gs == 64  ? launch_gemv<T, 2>(L, a, sms, stream)
+         : gs == 128 ? launch_gemv<T, 4>(L, a, sms, stream)
+                     : launch_gemv<T, 8>(L, a, sms, stream);
+}
+
+// Whether a launch's activations fit the streaming kernel's shared memory.
+bool gemv_fits(const flexq::W4Args& a) {
+  return a.K <= 65536 && flexq::gemv_smem(a.M, a.kbs, a.gs_shift) <= kGemvSmem;
+}
+
+// The batch kernel's columns are split over a cluster while its CTAs are fewer
+// than two per SM and every warp keeps at least two column tiles.
+int batch_split(long long ctas, int kbs, int sms) {
+  int ks = 1;
+  while (ks < 8 && ctas * ks < 2LL * sms && kbs >= 2 * ks * flexq::kBatchWarps) ks *= 2;
+  return ks;
 }
 
 template <typename T, int NT, int WPG>
-cudaError_t launch_gemv(const flexq::W4Layers& L, const flexq::GemvArgs& a, dim3 grid, cudaStream_t stream) {
+cudaError_t launch_batch(const flexq::W4Layers& L, const flexq::W4Args& a, dim3 grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(flexq::kGemvThreads);
+  cfg.blockDim = dim3(flexq::kBatchThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -62,23 +106,41 @@ cudaError_t launch_gemv(const flexq::W4Layers& L, const flexq::GemvArgs& a, dim3
   attr[0].val.clusterDim.z = grid.z;
   cfg.attrs = attr;
   cfg.numAttrs = grid.z > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, NT, kGemvStrips, WPG>, L, a);
+  return cudaLaunchKernelEx(&cfg, flexq::w4_batch_kernel<T, NT, kBatchStrips, WPG>, L, a);
 }
 
 template <typename T, int NT>
-cudaError_t launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::GemvArgs& a, dim3 grid,
-                           cudaStream_t stream) {
-  return gs == 32   ? launch_gemv<T, NT, 1>(L, a, grid, stream)
-         : gs == 64 ? launch_gemv<T, NT, 2>(L, a, grid, stream)
-                    : launch_gemv<T, NT, 4>(L, a, grid, stream);
+cudaError_t launch_batch_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, dim3 grid,
+                            cudaStream_t stream) {
+  return gs == 32   ? launch_batch<T, NT, 1>(L, a, grid, stream)
+         : gs == 64 ? launch_batch<T, NT, 2>(L, a, grid, stream)
+                    : launch_batch<T, NT, 4>(L, a, grid, stream);
 }
 
 template <typename T>
-cudaError_t launch_gemv_nt(int nt, int gs, const flexq::W4Layers& L, const flexq::GemvArgs& a,
-                           dim3 grid, cudaStream_t stream) {
-  return nt == 1   ? launch_gemv_gs<T, 1>(gs, L, a, grid, stream)
-         : nt == 2 ? launch_gemv_gs<T, 2>(gs, L, a, grid, stream)
-                   : launch_gemv_gs<T, 4>(gs, L, a, grid, stream);
+cudaError_t launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, int sms,
+                             cudaStream_t s) {
+  if (a.M <= kGemvTokens && gemv_fits(a)) return launch_gemv_gs<T>(gs, L, a, sms, s);
+  long long blocks = 0;
+  for (int l = 0; l < L.n; ++l) blocks += (L.strip0[l + 1] - L.strip0[l] + kBatchStrips - 1) / kBatchStrips;
+  const int tokens = a.M <= 16 ? 16 : 32;
+  const int tiles = (a.M + tokens - 1) / tokens;
+  const int ks = batch_split(blocks * tiles, a.kbs, sms);
+  // a grid's y extent ends at 65535: more tokens take several launches
+  for (int t0 = 0; t0 < tiles; t0 += 65535) {
+    const int n = std::min(65535, tiles - t0);
+    const long long m0 = static_cast<long long>(t0) * tokens;
+    flexq::W4Args at = a;
+    flexq::W4Layers Lt = L;
+    at.x = static_cast<const T*>(a.x) + m0 * a.ldx;
+    at.M = static_cast<int>(a.M - m0);
+    for (int l = 0; l < L.n; ++l) Lt.y[l] = static_cast<T*>(L.y[l]) + m0 * L.ldy[l];
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n), static_cast<unsigned>(ks));
+    const cudaError_t e = tokens == 16 ? launch_batch_gs<T, 2>(gs, Lt, at, grid, s)
+                                       : launch_batch_gs<T, 4>(gs, Lt, at, grid, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long ldx, int n_layers,
@@ -111,7 +173,7 @@ int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long l
   if ((rc = device_state(&st))) return rc;
 
   flexq::W4Layers L = {};
-  long long blocks = 0;
+  long long strips = 0;
   L.n = n_layers;
   for (int l = 0; l < n_layers; ++l) {
     L.wp[l] = static_cast<const uint4*>(layers[l].Wq_packed);
@@ -119,11 +181,11 @@ int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long l
     L.y[l] = layers[l].Y;
     L.ldy[l] = layers[l].ldy;
     L.N[l] = layers[l].N;
-    L.block0[l] = static_cast<int>(blocks);
-    blocks += (flexq::w4_row_tiles(layers[l].N) + kGemvStrips - 1) / kGemvStrips;
+    L.strip0[l] = static_cast<int>(strips);
+    strips += flexq::w4_row_tiles(layers[l].N);
   }
-  L.block0[n_layers] = static_cast<int>(blocks);
-  flexq::GemvArgs a = {};
+  L.strip0[n_layers] = static_cast<int>(strips);
+  flexq::W4Args a = {};
   a.x = X;
   a.ldx = ldx;
   a.M = M;
@@ -131,24 +193,15 @@ int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long l
   a.G = K / gs;
   a.kbs = flexq::w4_col_tiles(K);
   a.gs_shift = log2_gs(gs);
-  const GemvPlan p = gemv_plan(M, blocks, a.kbs, st->sms);
-  const int tiles = (M + 8 * p.nt - 1) / (8 * p.nt);
-  // a grid's y extent ends at 65535: more tokens take several launches
-  for (int t0 = 0; t0 < tiles; t0 += 65535) {
-    const int n = std::min(65535, tiles - t0);
-    flexq::GemvArgs at = a;
-    flexq::W4Layers Lt = L;
-    const long long m0 = static_cast<long long>(t0) * 8 * p.nt;
-    at.x = static_cast<const char*>(X) + 2 * m0 * ldx;
-    at.M = static_cast<int>(M - m0);
-    for (int l = 0; l < n_layers; ++l) Lt.y[l] = static_cast<char*>(L.y[l]) + 2 * m0 * L.ldy[l];
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n), static_cast<unsigned>(p.ks));
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == FLEXQ_DTYPE_FP16
-                              ? launch_gemv_nt<__half>(p.nt, gs, Lt, at, grid, s)
-                              : launch_gemv_nt<__nv_bfloat16>(p.nt, gs, Lt, at, grid, s);
-    if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
-  }
+  a.status = st->status;
+  a.wait_limit_ns = g_wait_limit_ns.load();
+  // the kernels number the 16 x 128 tiles of a launch in 32 bits
+  if (strips * a.kbs > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "%lld x %d weights are too many", strips * 16, K);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == FLEXQ_DTYPE_FP16
+                            ? launch_linear_w4<__half>(L, a, gs, st->sms, s)
+                            : launch_linear_w4<__nv_bfloat16>(L, a, gs, st->sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
   return ok();
 }
 

@@ -494,11 +494,30 @@ def linear_group(x, weights, group_size, act_bits=6, outs=None, workspace_buf=No
 
 
 # ------------------------------------------- 4-bit layers and packed tables --
+# These calls are short enough for the host's time to matter: arguments are
+# checked in one expression each, and taken apart (_need, _need_rows) only to
+# word a refusal.
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _need_rows(t, name, dtype, shape):
-    """A matrix whose rows are contiguous but may lie further apart."""
+def _is(t, dtype, shape, dev):
+    """A contiguous tensor of this type and shape on CUDA device `dev`."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous())
+
+
+def _refuse(t, name, dtype, shape, like):
+    _need(t, name, dtype, shape)
+    raise ValueError(f"tensors on {like.device} and {t.device}: all must share one device")
+
+
+def _is_rows(t, dtype, shape, dev):
+    """The same of a matrix whose rows are contiguous but may lie apart."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and (t.is_contiguous() or shape[1] <= 1 or t.stride(1) == 1))
+
+
+def _refuse_rows(t, name, dtype, shape, like):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -509,29 +528,46 @@ def _need_rows(t, name, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
+    raise ValueError(f"tensors on {like.device} and {t.device}: all must share one device")
 
 
-def _row_stride(t):
+def _row_stride(t, rows, cols):
     """Elements between rows (a single row has no stride of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+    return t.stride(0) if rows > 1 else cols
 
 
-def _same_device(x, *others):
-    for t in others:
-        if t is not None and t.device != x.device:
-            raise ValueError(f"tensors on {x.device} and {t.device}: all must share one device")
-
-
-def _activation_dtype(t, name):
+def _activation(t, name):
+    """(type, CUDA device index) of an FP16 or BF16 tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
-    return t.dtype
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    return t.dtype, t.get_device()
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, current stream of `dev`) with `dev` as the current device."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != FLEXQ_OK:
+        _check(status)
 
 
 def weight4_packed_bytes(N, K, group_size):
     return int(lib().flexq_weight4_packed_bytes(N, K, group_size))
+
+
+def _w4_bytes(N, K, group_size, what):
+    if N <= 0 or K <= 0 or group_size not in (32, 64, 128, 256) or K % group_size:
+        raise FlexQError(FLEXQ_ERR_UNSUPPORTED,
+                         f"unsupported {what} shape {N}x{K}, gs={group_size}")
+    return (N + 15) // 16 * ((K + 127) // 128) * 1024
 
 
 def quantize_weight4(w, group_size, out=None):
@@ -541,20 +577,42 @@ def quantize_weight4(w, group_size, out=None):
     if w.dim() != 2:
         raise ValueError(f"w must be [N, K], got {tuple(w.shape)}")
     N, K = w.shape
-    nbytes = weight4_packed_bytes(N, K, group_size)
-    if nbytes == 0:
-        raise FlexQError(FLEXQ_ERR_UNSUPPORTED, f"unsupported weight shape {N}x{K}, gs={group_size}")
+    nbytes, dev = _w4_bytes(N, K, group_size, "weight"), w.get_device()
     if out is None:
         out = (torch.empty(nbytes, dtype=torch.uint8, device=w.device),
                torch.empty(N, K // group_size, dtype=torch.float16, device=w.device))
     wp, ws = out
-    _need(wp, "packed", torch.uint8, (nbytes,))
-    _need(ws, "scales", torch.float16, (N, K // group_size))
-    _same_device(w, wp, ws)
-    with torch.cuda.device(w.device):
-        _check(lib().flexq_quantize_weight4(N, K, group_size, _ptr(w), _ptr(wp), _ptr(ws),
-                                            _stream(w)))
+    if not _is(wp, torch.uint8, (nbytes,), dev):
+        _refuse(wp, "packed", torch.uint8, (nbytes,), w)
+    if not _is(ws, torch.float16, (N, K // group_size), dev):
+        _refuse(ws, "scales", torch.float16, (N, K // group_size), w)
+    _launch(dev, lib().flexq_quantize_weight4, N, K, group_size, w.data_ptr(), wp.data_ptr(),
+            ws.data_ptr())
     return wp, ws
+
+
+def _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out):
+    """The checked output of a layer, and the distance of its rows."""
+    nbytes = _w4_bytes(N, K, group_size, "weight")
+    if not _is(wp, torch.uint8, (nbytes,), dev):
+        _refuse(wp, "wp", torch.uint8, (nbytes,), x)
+    if not _is(ws, torch.float16, (N, K // group_size), dev):
+        _refuse(ws, "ws", torch.float16, (N, K // group_size), x)
+    if out is None:
+        return torch.empty((M, N), dtype=dtype, device=x.device), N
+    if not _is_rows(out, dtype, (M, N), dev):
+        _refuse_rows(out, "out", dtype, (M, N), x)
+    return out, _row_stride(out, M, N)
+
+
+def _w4_input(x):
+    dtype, dev = _activation(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
+    M, K = x.shape
+    if not _is_rows(x, dtype, (M, K), dev):
+        _refuse_rows(x, "x", dtype, (M, K), x)
+    return dtype, dev, M, K, _row_stride(x, M, K)
 
 
 def linear4(x, wp, ws, N, group_size, out=None):
@@ -562,17 +620,17 @@ def linear4(x, wp, ws, N, group_size, out=None):
     BF16 activations x [M, K], which are not quantized; Y has x's type.  x and
     out may be views whose rows lie further apart (x: by a multiple of eight
     elements)."""
-    return linear4_group(x, [(wp, ws, N)], group_size, outs=[out])[0]
+    dtype, dev, M, K, ldx = _w4_input(x)
+    y, ldy = _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out)
+    _launch(dev, lib().flexq_linear_w4, M, N, K, group_size, _DTYPES[dtype], x.data_ptr(), ldx,
+            wp.data_ptr(), ws.data_ptr(), y.data_ptr(), ldy)
+    return y
 
 
 def linear4_group(x, weights, group_size, outs=None):
     """Layers [(wp, ws, N), ...] with 4-bit weights that read the same
     activations x [M, K] (1..4 layers), in one launch; returns their outputs."""
-    dtype = _activation_dtype(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
-    M, K = x.shape
-    _need_rows(x, "x", dtype, (M, K))
+    dtype, dev, M, K, ldx = _w4_input(x)
     if not 1 <= len(weights) <= MAX_GROUP_LAYERS:
         raise ValueError(f"1..{MAX_GROUP_LAYERS} layers, got {len(weights)}")
     if outs is not None and len(outs) != len(weights):
@@ -580,41 +638,35 @@ def linear4_group(x, weights, group_size, outs=None):
     arr = (Layer4 * len(weights))()
     ys = []
     for i, (wp, ws, N) in enumerate(weights):
-        nbytes = weight4_packed_bytes(N, K, group_size)
-        if nbytes == 0:
-            raise FlexQError(FLEXQ_ERR_UNSUPPORTED,
-                             f"unsupported weight shape {N}x{K}, gs={group_size}")
-        _need(wp, "wp", torch.uint8, (nbytes,))
-        _need(ws, "ws", torch.float16, (N, K // group_size))
-        y = outs[i] if outs is not None and outs[i] is not None else \
-            torch.empty(M, N, dtype=dtype, device=x.device)
-        _need_rows(y, "out", dtype, (M, N))
-        _same_device(x, wp, ws, y)
-        arr[i] = Layer4(N, wp.data_ptr(), ws.data_ptr(), y.data_ptr(), max(_row_stride(y), N))
+        y, ldy = _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev,
+                           None if outs is None else outs[i])
+        arr[i] = (N, wp.data_ptr(), ws.data_ptr(), y.data_ptr(), ldy)
         ys.append(y)
-    with torch.cuda.device(x.device):
-        _check(lib().flexq_linear_w4_group(M, K, group_size, _DTYPES[dtype], _ptr(x),
-                                           _row_stride(x), len(weights), arr, _stream(x)))
+    _launch(dev, lib().flexq_linear_w4_group, M, K, group_size, _DTYPES[dtype], x.data_ptr(), ldx,
+            len(weights), arr)
     return ys
 
 
-def _need_ids(ids):
+def _check_ids(ids):
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch.Tensor")
     if ids.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
-    _need(ids, "ids", ids.dtype)
-    return ids.element_size()
+    if not (ids.is_cuda and ids.is_contiguous()):
+        _need(ids, "ids", ids.dtype)
+    return ids.get_device(), 8 if ids.dtype is torch.int64 else 4
 
 
-def _need_table(wp, V, K, group_size, weight_bits):
-    if weight_bits not in (4, 6):
+def _table_bytes(V, K, group_size, weight_bits):
+    if weight_bits == 4:
+        return _w4_bytes(V, K, group_size, "table")
+    if weight_bits != 6:
         raise ValueError(f"weight_bits must be 4 or 6, got {weight_bits!r}")
-    nbytes = (weight4_packed_bytes if weight_bits == 4 else weight_packed_bytes)(V, K, group_size)
+    nbytes = weight_packed_bytes(V, K, group_size)
     if nbytes == 0:
         raise FlexQError(FLEXQ_ERR_UNSUPPORTED,
-                         f"unsupported table shape {V}x{K}, gs={group_size}, {weight_bits} bits")
-    _need(wp, "wp", torch.uint8, (nbytes,))
+                         f"unsupported table shape {V}x{K}, gs={group_size}, 6 bits")
+    return nbytes
 
 
 def _scales_shape(V, K, group_size, weight_bits):
@@ -627,25 +679,23 @@ def embedding(ids, wp, ws, V, group_size, scale=1.0, weight_bits=4, dtype=torch.
     each token of ids (int32 or int64, any shape), in FP16 or BF16.  wp, ws:
     quantize_weight4 (weight_bits 4) or quantize_weight (6, byte-aligned
     layout).  A token outside [0, V) is padding: its row is zero."""
-    id_bytes = _need_ids(ids)
+    dev, id_bytes = _check_ids(ids)
     if dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
-    if weight_bits not in (4, 6):
-        raise ValueError(f"weight_bits must be 4 or 6, got {weight_bits!r}")
-    _need(ws, "ws", torch.float16)
-    if ws.dim() != 2:
-        raise ValueError(f"ws must have two dimensions, got {tuple(ws.shape)}")
-    K = ws.shape[1 if weight_bits == 4 else 0] * group_size
-    _need_table(wp, V, K, group_size, weight_bits)
-    _need(ws, "ws", torch.float16, _scales_shape(V, K, group_size, weight_bits))
+    if not isinstance(ws, torch.Tensor) or ws.dim() != 2:
+        raise ValueError("ws must be a tensor with two dimensions")
+    K = ws.shape[0 if weight_bits == 6 else 1] * group_size
+    nbytes, shape = _table_bytes(V, K, group_size, weight_bits), (*ids.shape, K)
+    if not _is(wp, torch.uint8, (nbytes,), dev):
+        _refuse(wp, "wp", torch.uint8, (nbytes,), ids)
+    if not _is(ws, torch.float16, _scales_shape(V, K, group_size, weight_bits), dev):
+        _refuse(ws, "ws", torch.float16, _scales_shape(V, K, group_size, weight_bits), ids)
     if out is None:
-        out = torch.empty(*ids.shape, K, dtype=dtype, device=ids.device)
-    _need(out, "out", dtype, (*ids.shape, K))
-    _same_device(ids, wp, ws, out)
-    with torch.cuda.device(ids.device):
-        _check(lib().flexq_embedding(ids.numel(), V, K, group_size, weight_bits, _DTYPES[dtype],
-                                     _ptr(ids), id_bytes, _ptr(wp), _ptr(ws), float(scale),
-                                     _ptr(out), _stream(ids)))
+        out = torch.empty(shape, dtype=dtype, device=ids.device)
+    elif not _is(out, dtype, shape, dev):
+        _refuse(out, "out", dtype, shape, ids)
+    _launch(dev, lib().flexq_embedding, ids.numel(), V, K, group_size, weight_bits, _DTYPES[dtype],
+            ids.data_ptr(), id_bytes, wp.data_ptr(), ws.data_ptr(), scale, out.data_ptr())
     return out
 
 
@@ -666,13 +716,16 @@ def embedding_backward(dy, ids, wp, V, group_size, scale=1.0, weight_bits=4, tab
     workspace_buf: a uint8 device tensor of at least
                    embedding_backward_workspace_bytes(tokens, K) bytes that no
                    other running call uses; by default one of this call's own."""
-    dtype = _activation_dtype(dy, "dy")
-    id_bytes = _need_ids(ids)
+    dtype, dev = _activation(dy, "dy")
+    ids_dev, id_bytes = _check_ids(ids)
     if dy.dim() < 1:
         raise ValueError("dy must be [..., K]")
     T, K = ids.numel(), dy.shape[-1]
-    _need(dy, "dy", dtype, (*ids.shape, K))
-    _need_table(wp, V, K, group_size, weight_bits)
+    if not _is(dy, dtype, (*ids.shape, K), ids_dev):
+        _refuse(dy, "dy", dtype, (*ids.shape, K), ids)
+    nbytes = _table_bytes(V, K, group_size, weight_bits)
+    if not _is(wp, torch.uint8, (nbytes,), dev):
+        _refuse(wp, "wp", torch.uint8, (nbytes,), dy)
     if table_dtype not in (None, dtype, torch.float32):
         raise ValueError(f"table_dtype must be {dtype} or torch.float32, got {table_dtype}")
     if table_dtype is None and not with_scales:
@@ -680,27 +733,26 @@ def embedding_backward(dy, ids, wp, V, group_size, scale=1.0, weight_bits=4, tab
     table, scales = out if out is not None else (None, None)
     if table_dtype is None:
         table = None
-    else:
-        if table is None:
-            table = torch.empty(V, K, dtype=table_dtype, device=dy.device)
-        _need(table, "rows", table_dtype, (V, K))
+    elif table is None:
+        table = torch.empty((V, K), dtype=table_dtype, device=dy.device)
+    elif not _is(table, table_dtype, (V, K), dev):
+        _refuse(table, "rows", table_dtype, (V, K), dy)
     shape = _scales_shape(V, K, group_size, weight_bits)
     if not with_scales:
         scales = None
-    else:
-        if scales is None:
-            scales = torch.empty(shape, dtype=torch.float32, device=dy.device)
-        _need(scales, "scales", torch.float32, shape)
+    elif scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=dy.device)
+    elif not _is(scales, torch.float32, shape, dev):
+        _refuse(scales, "scales", torch.float32, shape, dy)
     if workspace_buf is None:
         workspace_buf = torch.empty(embedding_backward_workspace_bytes(T, K), dtype=torch.uint8,
                                     device=dy.device)
-    _need(workspace_buf, "workspace", torch.uint8)
-    _same_device(dy, ids, wp, table, scales, workspace_buf)
-    with torch.cuda.device(dy.device):
-        _check(lib().flexq_embedding_backward(
-            T, V, K, group_size, weight_bits, _DTYPES[dtype], _ptr(ids), id_bytes, _ptr(dy),
-            _ptr(wp), float(scale), _DTYPES[table_dtype] if table is not None else 0,
-            _ptr(table) if table is not None else None,
-            _ptr(scales) if scales is not None else None, _ptr(workspace_buf),
-            workspace_buf.numel(), _stream(dy)))
+    elif not _is(workspace_buf, torch.uint8, (workspace_buf.numel(),), dev):
+        _refuse(workspace_buf, "workspace", torch.uint8, (workspace_buf.numel(),), dy)
+    _launch(dev, lib().flexq_embedding_backward, T, V, K, group_size, weight_bits, _DTYPES[dtype],
+            ids.data_ptr(), id_bytes, dy.data_ptr(), wp.data_ptr(), scale,
+            _DTYPES[table_dtype] if table is not None else 0,
+            None if table is None else table.data_ptr(),
+            None if scales is None else scales.data_ptr(), workspace_buf.data_ptr(),
+            workspace_buf.numel())
     return table, scales

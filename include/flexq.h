@@ -392,8 +392,8 @@ size_t flexq_weight4_packed_bytes(int N, int K, int group_size);
  *                 1024 bytes at (nt * ceil(K/128) + kb) * 1024; row r is 64
  *                 bytes at 64 r; 16-byte chunk t of it holds four
  *                 little-endian words, word w the codes of columns 32 w + 8 t
- *                 + i (i = 0..7) as u = q + 8 in nibble i/2 + 4 (i%2).  Rows
- *                 past N and columns past K hold u = 8.
+ *                 + i (i = 0..7) as u = q + 8, in nibbles 0, 4, 2, 6, 1, 5, 3,
+ *                 7 in this order.  Rows past N and columns past K hold u = 8.
  *   W_scales_fp16 out, FP16 [N, G] row-major (unlike the group-major scales of
  *                 the 6-bit form: a row's scales are read together here).
  */

@@ -42,7 +42,7 @@ def test_the_packed_form_by_plain_index_arithmetic():
         tile = (n // 16) * 3 + k // 128
         kk, r = k % 128, n % 16
         w, t, i = kk // 32, kk // 8 % 4, kk % 8
-        nibble = i // 2 + 4 * (i % 2)
+        nibble = [0, 4, 2, 6, 1, 5, 3, 7][i]
         byte = b[tile * 1024 + r * 64 + t * 16 + w * 4 + nibble // 2]
         assert (int(byte) >> (4 * (nibble % 2))) & 15 == q[n, k] + 8
     assert np.array_equal(unpack4(b, N, K), q)

@@ -16,6 +16,9 @@ def quantize4(w16, gs):
     return q.reshape(w16.shape).astype(np.int8), s
 
 
+NIBBLES = (0, 4, 2, 6, 1, 5, 3, 7)           # of a word's eight columns
+
+
 def pack4(q):
     """The packed bytes of codes [N, K] in -8 .. 7."""
     N, K = q.shape
@@ -26,7 +29,7 @@ def pack4(q):
     u = u.reshape(Np // 16, 16, Kp // 128, 4, 4, 8)
     words = np.zeros(u.shape[:-1], dtype=np.uint32)
     for i in range(8):
-        words |= u[..., i] << np.uint32(4 * (i // 2 + 4 * (i % 2)))
+        words |= u[..., i] << np.uint32(4 * NIBBLES[i])
     # -> [row tile, column tile, row, chunk, word]
     return np.ascontiguousarray(words.transpose(0, 2, 1, 4, 3)).astype("<u4").view(np.uint8).reshape(-1)
 
@@ -35,7 +38,7 @@ def unpack4(b, N, K):
     """The codes [N, K] of packed bytes."""
     rt, ct = -(-N // 16), -(-K // 128)
     words = b.view("<u4").reshape(rt, ct, 16, 4, 4).transpose(0, 2, 1, 4, 3)
-    q = np.stack([(words >> np.uint32(4 * (i // 2 + 4 * (i % 2)))) & 15 for i in range(8)], axis=-1)
+    q = np.stack([(words >> np.uint32(4 * NIBBLES[i])) & 15 for i in range(8)], axis=-1)
     return (q.astype(np.int64) - 8).astype(np.int8).reshape(rt * 16, ct * 128)[:N, :K]
 
 

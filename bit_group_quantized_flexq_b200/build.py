@@ -14,8 +14,8 @@ SRC = os.path.join(PKG, "csrc", "flexq_lib.cu")
 LIB = os.path.join(PKG, "libflexq.so")
 DEPS = [os.path.join(PKG, "csrc", f) for f in
         ("flexq_lib.cu", "flexq_api.cu", "flexq_gemm.cuh", "flexq_gemm_wide.cuh",
-         "flexq_quant.cuh", "flexq_ptx.cuh", "flexq_w4.cuh", "flexq_embed.cuh",
-         "flexq_w4_api.cuh")] + \
+         "flexq_quant.cuh", "flexq_ptx.cuh", "flexq_w4.cuh", "flexq_w4_gemm.cuh",
+         "flexq_embed.cuh", "flexq_w4_api.cuh")] + \
        [os.path.join(ROOT, "include", "flexq.h")]
 
 NVCC_FLAGS = [

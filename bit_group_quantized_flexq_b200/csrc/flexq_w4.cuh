@@ -568,147 +568,4 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   cluster_sync_all();               // no CTA leaves while another reads its part
 }
 
-// -------------------------------------------------------- larger batches --
-constexpr int kBatchWarps = 8;
-constexpr int kBatchThreads = kBatchWarps * 32;
-
-// Registers of one step: a 16 x 128 tile per strip and the batch's
-// activations for its columns.
-template <int NT, int S>
-struct BatchStep {
-  uint4 w[S][2];                  // rows g and g + 8 of each strip
-  uint4 x[NT][4];                 // per word: eight columns of token g
-};
-
-// One CTA: S * 16 rows of one layer, all of K (or its cluster rank's share),
-// NT * 8 tokens.  The warps take the tiles of 128 columns in turn; each
-// multiplies its codes (exact in FP16 and BF16) with the activations on the
-// tensor core in FP32 and adds a group's sum times the scale, in FP32, to its
-// totals.  The warps' totals are added in shared memory, the cluster's in
-// distributed shared memory, always in the same order.
-template <typename T, int NT, int S, int WPG>
-__global__ void __launch_bounds__(kBatchThreads) w4_batch_kernel(const __grid_constant__ W4Layers L,
-                                                              const W4Args a) {
-  constexpr int kRows = 16 * S, kTok = 8 * NT;
-  __shared__ float red[kBatchWarps][S * NT * 4][32];
-  __shared__ float tot[kRows * kTok];
-  // the layer that the block's number falls into, S strips to a block
-  int l = 0, block = blockIdx.x;
-  while (l + 1 < L.n && block >= (L.strip0[l + 1] - L.strip0[l] + S - 1) / S) {
-    block -= (L.strip0[l + 1] - L.strip0[l] + S - 1) / S;
-    ++l;
-  }
-  const int strip0 = block * S;
-  const int N = L.N[l], strips = w4_row_tiles(N);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int m0 = blockIdx.y * kTok;
-  const int ks = gridDim.z, rank = blockIdx.z;
-  const T* x = static_cast<const T*>(a.x);
-  const uint4* wp = L.wp[l] + static_cast<size_t>(strip0) * a.kbs * (kW4TileBytes / 16);
-  const __half* ws = L.ws[l];
-
-  float acc[S][NT][4] = {};
-  auto load = [&](BatchStep<NT, S>& st, int kb) {
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const bool in = strip0 + s < strips;
-      const uint4* p = wp + (static_cast<size_t>(s) * a.kbs + kb) * (kW4TileBytes / 16) + lane;
-      const uint4 zero = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-      st.w[s][0] = in ? __ldcs(p) : zero;
-      st.w[s][1] = in ? __ldcs(p + 32) : zero;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int m = m0 + nt * 8 + g;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int k = kb * 128 + w * 32 + t * 8;
-        st.x[nt][w] = (m < a.M && k < a.K)
-                          ? __ldg(reinterpret_cast<const uint4*>(x + m * a.ldx + k))
-                          : make_uint4(0, 0, 0, 0);
-      }
-    }
-  };
-  const int stride = kBatchWarps * ks;
-  int kb = rank * kBatchWarps + warp;
-  BatchStep<NT, S> cur, nxt;
-  if (kb < a.kbs) load(cur, kb);
-  for (; kb < a.kbs; kb += stride) {
-    if (kb + stride < a.kbs) load(nxt, kb + stride);
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int row = (strip0 + s) * 16 + g;
-      float part[NT][4] = {};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t lo[4], hi[4];
-        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&cur.w[s][0]);
-        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&cur.w[s][1]);
-        Elem<T>::codes(w0[w], lo);
-        Elem<T>::codes(w1[w], hi);
-        const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
-        const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Elem<T>::mma(part[nt], a0, cur.x[nt][w].x, cur.x[nt][w].y, part[nt]);
-          Elem<T>::mma(part[nt], a1, cur.x[nt][w].z, cur.x[nt][w].w, part[nt]);
-        }
-        if ((w + 1) % WPG == 0) {
-          const int k = kb * 128 + w * 32;
-          const int grp = k >> a.gs_shift;
-          const float s0 = (row < N && k < a.K)
-                               ? __half2float(__ldg(ws + static_cast<size_t>(row) * a.G + grp)) : 0.0f;
-          const float s1 = (row + 8 < N && k < a.K)
-                               ? __half2float(__ldg(ws + static_cast<size_t>(row + 8) * a.G + grp)) : 0.0f;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            acc[s][nt][0] = fmaf(part[nt][0], s0, acc[s][nt][0]);
-            acc[s][nt][1] = fmaf(part[nt][1], s0, acc[s][nt][1]);
-            acc[s][nt][2] = fmaf(part[nt][2], s1, acc[s][nt][2]);
-            acc[s][nt][3] = fmaf(part[nt][3], s1, acc[s][nt][3]);
-            part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.0f;
-          }
-        }
-      }
-    }
-    cur = nxt;
-  }
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[warp][(s * NT + nt) * 4 + i][lane] = acc[s][nt][i];
-  __syncthreads();
-  // tot[token][row]: value i of lane (g, t) is row g + 8 (i / 2), token 2 t + i % 2
-  for (int o = threadIdx.x; o < kRows * kTok; o += kBatchThreads) {
-    const int row = o % kRows, tok = o / kRows;
-    const int s = row >> 4, nt = tok >> 3;
-    const int i = ((row >> 3) & 1) * 2 + (tok & 1), ln = (row & 7) * 4 + ((tok & 7) >> 1);
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kBatchWarps; ++w) v += red[w][(s * NT + nt) * 4 + i][ln];
-    tot[o] = v;
-  }
-  if (ks > 1) cluster_sync_all(); else __syncthreads();
-  // the cluster's CTAs share the outputs; each adds the ranks' totals in order
-  T* y = static_cast<T*>(L.y[l]);
-  for (int o = rank * kBatchThreads + threadIdx.x; o < kRows * kTok; o += kBatchThreads * ks) {
-    const int row = strip0 * 16 + o % kRows, m = m0 + o / kRows;
-    float v = 0.0f;
-    if (ks == 1) {
-      v = tot[o];
-    } else {
-      for (int r = 0; r < ks; ++r) {
-        const uint32_t p = map_to_rank(smem_u32(&tot[o]), r);
-        float u;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(p) : "memory");
-        v += u;
-      }
-    }
-    if (row < N && m < a.M) y[m * L.ldy[l] + row] = Elem<T>::from_float(v);
-  }
-  if (ks > 1) cluster_sync_all();   // no CTA leaves while another reads its totals
-}
-
 }  // namespace flexq

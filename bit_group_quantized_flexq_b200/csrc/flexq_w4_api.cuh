@@ -4,6 +4,7 @@
 
 #include "flexq_embed.cuh"
 #include "flexq_w4.cuh"
+#include "flexq_w4_gemm.cuh"
 
 namespace {
 
@@ -31,7 +32,6 @@ size_t w4_packed_bytes(int N, int K) {
 // ----------------------------------------------------------- linear layers --
 constexpr int kGemvTokens = 8;    // batches of the streaming kernel
 constexpr int kGemvSmem = 208 * 1024;   // its buffers, activations and their sums
-constexpr int kBatchStrips = 2;   // 16-row strips per CTA of the batch kernel
 
 // Lets a kernel use more than 48 KB of shared memory, once per device.
 template <typename Kernel>
@@ -85,62 +85,140 @@ bool gemv_fits(const flexq::W4Args& a) {
   return a.K <= 65536 && flexq::gemv_smem(a.M, a.kbs, a.gs_shift) <= kGemvSmem;
 }
 
-// The batch kernel's columns are split over a cluster while its CTAs are fewer
-// than two per SM and every warp keeps at least two column tiles.
-int batch_split(long long ctas, int kbs, int sms) {
-  int ks = 1;
-  while (ks < 8 && ctas * ks < 2LL * sms && kbs >= 2 * ks * flexq::kBatchWarps) ks *= 2;
-  return ks;
+// ---- batches beyond those: the tcgen05 kernel ----
+// FP16 or BF16 activations [M, K], rows ldx apart; box = 64 columns (128
+// bytes, swizzled) x T rows.  Rows past M and columns past K read as zero.
+int encode_w4_x_map(CUtensorMap* map, const void* x, int dtype, int M, int K, long long ldx, int T) {
+  auto fn = encode_fn();
+  if (!fn) return fail(FLEXQ_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(M)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldx) * 2};
+  cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(T)};
+  cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = fn(map, dtype == FLEXQ_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        2, const_cast<void*>(x), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FLEXQ_ERR_CUDA, "cuTensorMapEncodeTiled (X) failed (%d)", static_cast<int>(r));
+  return FLEXQ_OK;
 }
 
-template <typename T, int NT, int WPG>
-cudaError_t launch_batch(const flexq::W4Layers& L, const flexq::W4Args& a, dim3 grid, cudaStream_t stream) {
+// The packed form as strips of 16 kbs rows of 64 bytes; box = one tile of 128
+// columns of eight strips, 64-byte swizzle.  Strips past the last read as zero.
+int encode_w4_map(CUtensorMap* map, const void* wp, int N, int kbs) {
+  auto fn = encode_fn();
+  if (!fn) return fail(FLEXQ_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[3] = {16u, static_cast<cuuint64_t>(kbs) * 16, static_cast<cuuint64_t>(flexq::w4_row_tiles(N))};
+  cuuint64_t strides[2] = {64u, static_cast<cuuint64_t>(kbs) * flexq::kW4TileBytes};
+  cuuint32_t box[3] = {16u, 16u, 8u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(wp), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(FLEXQ_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit weights) failed (%d)", static_cast<int>(r));
+  return FLEXQ_OK;
+}
+
+cudaLaunchConfig_t w4_mma_config(int smem, long long ctas, int split, cudaLaunchAttribute (&attr)[2],
+                                 cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(flexq::kBatchThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(flexq::kW4MmaThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = grid.z;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = grid.z > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, flexq::w4_batch_kernel<T, NT, kBatchStrips, WPG>, L, a);
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cfg;
 }
 
-template <typename T, int NT>
-cudaError_t launch_batch_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, dim3 grid,
-                            cudaStream_t stream) {
-  return gs == 32   ? launch_batch<T, NT, 1>(L, a, grid, stream)
-         : gs == 64 ? launch_batch<T, NT, 2>(L, a, grid, stream)
-                    : launch_batch<T, NT, 4>(L, a, grid, stream);
-}
-
-template <typename T>
-cudaError_t launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, int sms,
-                             cudaStream_t s) {
-  if (a.M <= kGemvTokens && gemv_fits(a)) return launch_gemv_gs<T>(gs, L, a, sms, s);
-  long long blocks = 0;
-  for (int l = 0; l < L.n; ++l) blocks += (L.strip0[l + 1] - L.strip0[l] + kBatchStrips - 1) / kBatchStrips;
-  const int tokens = a.M <= 16 ? 16 : 32;
-  const int tiles = (a.M + tokens - 1) / tokens;
-  const int ks = batch_split(blocks * tiles, a.kbs, sms);
-  // a grid's y extent ends at 65535: more tokens take several launches
-  for (int t0 = 0; t0 < tiles; t0 += 65535) {
-    const int n = std::min(65535, tiles - t0);
-    const long long m0 = static_cast<long long>(t0) * tokens;
-    flexq::W4Args at = a;
-    flexq::W4Layers Lt = L;
-    at.x = static_cast<const T*>(a.x) + m0 * a.ldx;
-    at.M = static_cast<int>(a.M - m0);
-    for (int l = 0; l < L.n; ++l) Lt.y[l] = static_cast<T*>(L.y[l]) + m0 * L.ldy[l];
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n), static_cast<unsigned>(ks));
-    const cudaError_t e = tokens == 16 ? launch_batch_gs<T, 2>(gs, Lt, at, grid, s)
-                                       : launch_batch_gs<T, 4>(gs, Lt, at, grid, s);
-    if (e != cudaSuccess) return e;
+// How many clusters of `split` CTAs run at once (asked once per device).
+template <typename E, int T>
+int w4_mma_clusters(int split, int* clusters) {
+  static int known[kMaxDevices][9];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  {
+    std::lock_guard<std::mutex> lock(g_dev_mutex);
+    *clusters = known[dev][split];
   }
-  return cudaSuccess;
+  if (*clusters > 0) return FLEXQ_OK;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = w4_mma_config(flexq::W4MmaCfg<T>::kSmem, split, split, attr, nullptr);
+  cfg.attrs = attr + 1;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(clusters, flexq::w4_mma_kernel<E, T>, &cfg);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+  *clusters = std::max(1, *clusters);
+  std::lock_guard<std::mutex> lock(g_dev_mutex);
+  known[dev][split] = *clusters;
+  return FLEXQ_OK;
+}
+
+template <typename E, int T>
+int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, long long ldx, int sms,
+                  cudaStream_t stream) {
+  constexpr int dtype = std::is_same<E, __half>::value ? FLEXQ_DTYPE_FP16 : FLEXQ_DTYPE_BF16;
+  static bool ready[kMaxDevices];
+  cudaError_t e = allow_smem(flexq::w4_mma_kernel<E, T>, flexq::W4MmaCfg<T>::kSmem, ready);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  int rc = encode_w4_x_map(&a.x, x, dtype, a.M, a.K, ldx, T);
+  for (int l = 0; !rc && l < L.n; ++l) rc = encode_w4_map(&a.w[l], L.wp[l], L.N[l], a.kbs);
+  if (rc) return rc;
+  a.token_tiles = (a.M + T - 1) / T;
+  const long long tiles = static_cast<long long>(a.tile0[L.n]) * a.token_tiles;
+  // a tile's columns are shared by as many CTAs as still run in one wave, each
+  // with at least four column tiles
+  a.split = 1;
+  for (int s = 2; s <= 8 && tiles * s <= 2LL * sms && a.kbs >= 4 * s; s *= 2) {
+    int clusters = 0;
+    if ((rc = w4_mma_clusters<E, T>(s, &clusters))) return rc;
+    if (tiles > clusters) break;
+    a.split = s;
+  }
+  if (tiles * a.split > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d with %d weight rows too large", a.M, a.tile0[L.n] * 128);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = w4_mma_config(flexq::W4MmaCfg<T>::kSmem, tiles * a.split, a.split, attr, stream);
+  e = cudaLaunchKernelEx(&cfg, flexq::w4_mma_kernel<E, T>, a);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
+  return FLEXQ_OK;
+}
+
+template <typename E>
+int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, int sms, cudaStream_t s) {
+  if (a.M <= kGemvTokens && gemv_fits(a)) {
+    const cudaError_t e = launch_gemv_gs<E>(gs, L, a, sms, s);
+    return e == cudaSuccess ? FLEXQ_OK : cuda_fail(e, "4-bit linear launch");
+  }
+  flexq::W4MmaArgs m;
+  memset(&m, 0, sizeof(m));
+  m.n = L.n;
+  for (int l = 0; l < L.n; ++l) {
+    m.ws[l] = L.ws[l];
+    m.y[l] = L.y[l];
+    m.ldy[l] = L.ldy[l];
+    m.N[l] = L.N[l];
+    m.tile0[l + 1] = m.tile0[l] + (L.N[l] + flexq::kW4MmaRows - 1) / flexq::kW4MmaRows;
+  }
+  m.M = a.M;
+  m.K = a.K;
+  m.G = a.G;
+  m.kbs = a.kbs;
+  m.gs_shift = a.gs_shift;
+  m.status = a.status;
+  m.wait_limit_ns = a.wait_limit_ns;
+  return a.M <= 16   ? launch_w4_mma<E, 16>(m, L, a.x, a.ldx, sms, s)
+         : a.M <= 32 ? launch_w4_mma<E, 32>(m, L, a.x, a.ldx, sms, s)
+         : a.M <= 64 ? launch_w4_mma<E, 64>(m, L, a.x, a.ldx, sms, s)
+                     : launch_w4_mma<E, 128>(m, L, a.x, a.ldx, sms, s);
 }
 
 int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long ldx, int n_layers,
@@ -198,11 +276,9 @@ int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long l
   // the kernels number the 16 x 128 tiles of a launch in 32 bits
   if (strips * a.kbs > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "%lld x %d weights are too many", strips * 16, K);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == FLEXQ_DTYPE_FP16
-                            ? launch_linear_w4<__half>(L, a, gs, st->sms, s)
-                            : launch_linear_w4<__nv_bfloat16>(L, a, gs, st->sms, s);
-  if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
-  return ok();
+  rc = dtype == FLEXQ_DTYPE_FP16 ? launch_linear_w4<__half>(L, a, gs, st->sms, s)
+                                 : launch_linear_w4<__nv_bfloat16>(L, a, gs, st->sms, s);
+  return rc ? rc : ok();
 }
 
 // ------------------------------------------------------------------ tables --

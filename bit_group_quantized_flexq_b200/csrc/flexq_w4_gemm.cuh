@@ -1,0 +1,375 @@
+// flexq_w4_gemm.cuh -- 4-bit linear layers for batches beyond the streaming
+// kernel's, on the tensor core's tcgen05 MMA.
+//
+// One CTA: 128 weight rows x T tokens over its share of the columns.  The
+// weights are the MMA's A operand, in tensor memory: unpack warps turn a tile
+// of 128 rows x 128 columns (8 KB of codes, one TMA box) into FP16 or BF16
+// values and store them there; the activations are the B operand, in shared
+// memory as TMA brings them; one FP32 accumulator of T columns takes the whole
+// share.  An unpacked weight is the rounded product of code and scale, half a
+// step of the activations' type: keeping the codes whole and scaling each
+// group's sum instead would read the accumulator back once per group, which
+// costs a tile of 128 tokens more time than its MMAs.
+//
+// With fewer tiles than the machine has room for, a cluster of CTAs shares a
+// tile's columns; each leaves its sums in its shared memory, and the CTAs add
+// them up in the order of the columns, a share of the tokens each.
+#pragma once
+
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "flexq_gemm.cuh"
+#include "flexq_w4.cuh"
+
+namespace flexq {
+
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, "
+      "p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u),
+      "r"(0u), "r"(0u)
+      : "memory");
+}
+
+// Instruction descriptor: FP16 or BF16 operands, FP32 accumulator, both
+// K-major, M x N.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  constexpr uint32_t ab = std::is_same<T, __half>::value ? 0u : 1u;
+  return (1u << 4) | (ab << 7) | (ab << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// A row's scale for one group, ready for its codes.
+template <typename T>
+struct RowScale;
+
+template <>
+struct RowScale<__half> {
+  __half2 s;
+  __device__ __forceinline__ explicit RowScale(uint32_t bits)
+      : s(__half2half2(__ushort_as_half(static_cast<unsigned short>(bits)))) {}
+  // eight codes of a word -> four pairs code * scale, each rounded once
+  __device__ __forceinline__ void apply(uint32_t w, uint32_t* out) const {
+    uint32_t p[4];
+    Elem<__half>::codes(w, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[i]), s);
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+
+template <>
+struct RowScale<__nv_bfloat16> {
+  // an FP16 scale as a sum of two BF16 values (11 bits of mantissa in 8 + 8)
+  __nv_bfloat162 hi, lo;
+  __device__ __forceinline__ explicit RowScale(uint32_t bits) {
+    const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    const __nv_bfloat16 h = __float2bfloat16_rn(f);
+    hi = __bfloat162bfloat162(h);
+    lo = __bfloat162bfloat162(__float2bfloat16_rn(f - __bfloat162float(h)));
+  }
+  // code * lo is exact (4 + 3 bits), so the sum rounds code * scale once
+  __device__ __forceinline__ void apply(uint32_t w, uint32_t* out) const {
+    uint32_t p[4];
+    Elem<__nv_bfloat16>::codes(w, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 q = *reinterpret_cast<const __nv_bfloat162*>(&p[i]);
+      const __nv_bfloat162 v = __hfma2(q, hi, __hmul2(q, lo));
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+
+constexpr int kW4MmaThreads = 256;      // warps 0 producer, 1 MMA, 2-3 idle, 4-7 unpack + epilogue
+constexpr int kW4MmaRows = 128;
+constexpr int kW4MmaTileBytes = 8 * kW4TileBytes;
+
+template <int T>
+struct W4MmaCfg {
+  static constexpr int kXBox = T * 128;                 // 64 columns of T tokens
+  static constexpr int kXSlot = 2 * kXBox;
+  static constexpr int kXSlots = T == 128 ? 2 : T == 64 ? 4 : T == 32 ? 6 : 8;
+  static constexpr int kWSlots = T == 128 ? 4 : T == 16 ? 6 : 5;
+  static constexpr int kXBytes = kXSlots * kXSlot;
+  static constexpr int kWBytes = kWSlots * kW4MmaTileBytes;
+  // the sums a CTA leaves for its cluster lie over the operand slots
+  static constexpr int kMain = kXBytes + kWBytes > T * kW4MmaRows * 4 ? kXBytes + kWBytes
+                                                                     : T * kW4MmaRows * 4;
+  static constexpr int kSmem = kMain + 1024;            // aligned to the swizzle's 1024 bytes
+  static constexpr int kAccCols = T < 32 ? 32 : T;
+  static constexpr int kACols = 64;                     // 128 columns of weights
+  static constexpr int kASlots = 2;
+  static constexpr int kTmemCols = 256;                 // two CTAs share an SM's 512
+  static_assert(kAccCols + kASlots * kACols <= kTmemCols, "tensor memory");
+  // a third CTA on the SM would wait for tensor memory
+  static_assert(3 * kSmem > 227 * 1024 && 2 * (kSmem + 2048) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct W4MmaArgs {
+  CUtensorMap x;                        // [M][K], boxes of 64 columns x T tokens, 128-byte swizzle
+  CUtensorMap w[kW4MaxLayers];          // [strip][16 kbs rows][64 bytes], boxes of 8 strips, 64-byte swizzle
+  const __half* ws[kW4MaxLayers];
+  void* y[kW4MaxLayers];
+  long long ldy[kW4MaxLayers];
+  int N[kW4MaxLayers];
+  int tile0[kW4MaxLayers + 1];          // first tile of 128 rows of each layer
+  int n;
+  int M, K, G, kbs, gs_shift;
+  int split;                            // CTAs of a cluster, which share a tile's columns
+  int token_tiles;
+  unsigned int* status;
+  unsigned long long wait_limit_ns;
+};
+
+template <typename E, int T>
+__global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_constant__ W4MmaArgs a) {
+  using Cfg = W4MmaCfg<T>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t x_full[Cfg::kXSlots], x_empty[Cfg::kXSlots];
+  __shared__ uint64_t w_full[Cfg::kWSlots], w_empty[Cfg::kWSlots];
+  __shared__ uint64_t a_full[Cfg::kASlots], a_empty[Cfg::kASlots];
+  __shared__ uint64_t acc_full;
+  __shared__ uint32_t tmem_at;
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* x_mem = base;
+  uint8_t* w_mem = base + Cfg::kXBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t lim = a.wait_limit_ns;
+
+  // the tile: token tiles vary fastest, so that the CTAs in flight share weights
+  const int rank = blockIdx.x % a.split, tile = blockIdx.x / a.split;
+  const int mt = tile % a.token_tiles, rt = tile / a.token_tiles;
+  int l = 0;
+  while (l + 1 < a.n && rt >= a.tile0[l + 1]) ++l;
+  const int strip0 = (rt - a.tile0[l]) * 8;
+  const int kb0 = static_cast<int>(static_cast<long long>(rank) * a.kbs / a.split);
+  const int nk = static_cast<int>(static_cast<long long>(rank + 1) * a.kbs / a.split) - kb0;
+
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < Cfg::kXSlots; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&x_empty[i], 1);
+    }
+    for (int i = 0; i < Cfg::kWSlots; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 4);
+    }
+    for (int i = 0; i < Cfg::kASlots; ++i) {
+      mbar_init(&a_full[i], 4);
+      mbar_init(&a_empty[i], 1);
+    }
+    mbar_init(&acc_full, 1);
+    fence_barrier_init();
+  }
+  auto load_w = [&](int i) {
+    uint64_t* bar = &w_full[i % Cfg::kWSlots];
+    mbar_arrive_expect_tx(bar, kW4MmaTileBytes);
+    tma_load_3d(w_mem + i % Cfg::kWSlots * kW4MmaTileBytes, &a.w[l], bar, 0, (kb0 + i) * 16, strip0);
+  };
+  auto load_x = [&](int i) {
+    uint64_t* bar = &x_full[i % Cfg::kXSlots];
+    uint8_t* dst = x_mem + i % Cfg::kXSlots * Cfg::kXSlot;
+    mbar_arrive_expect_tx(bar, Cfg::kXSlot);
+    tma_load_2d(dst, &a.x, bar, (kb0 + i) * 128, mt * T);
+    tma_load_2d(dst + Cfg::kXBox, &a.x, bar, (kb0 + i) * 128 + 64, mt * T);
+  };
+  if (warp == 0 && lane == 0)           // the weights are constants: before the wait below
+    for (int i = 0; i < Cfg::kWSlots && i < nk; ++i) load_w(i);
+  if (warp == 1) tmem_alloc(&tmem_at, Cfg::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  const uint32_t acc_col = tmem, a_col0 = tmem + Cfg::kAccCols;
+  grid_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------- producer -----
+    if (lane == 0) {
+      grid_wait_dependencies();
+      for (int i = 0; i < Cfg::kXSlots && i < nk; ++i) load_x(i);
+      int w_issued = min(nk, Cfg::kWSlots), x_issued = min(nk, Cfg::kXSlots);
+      bool ok = true;
+      for (int i = 0; ok && i < nk; ++i) {
+        if (i + Cfg::kWSlots < nk) {
+          ok = mbar_wait(&w_empty[i % Cfg::kWSlots], (i / Cfg::kWSlots) & 1, lim);
+          if (ok) {
+            load_w(i + Cfg::kWSlots);
+            ++w_issued;
+          }
+        }
+        if (ok && i + Cfg::kXSlots < nk) {
+          ok = mbar_wait(&x_empty[i % Cfg::kXSlots], (i / Cfg::kXSlots) & 1, lim);
+          if (ok) {
+            load_x(i + Cfg::kXSlots);
+            ++x_issued;
+          }
+        }
+      }
+      if (!ok) record_status(a.status, kStatusTimeout, 0);
+      // every issued copy must land before the CTA may finish
+      for (int i = max(0, w_issued - Cfg::kWSlots); i < w_issued; ++i)
+        mbar_wait(&w_full[i % Cfg::kWSlots], (i / Cfg::kWSlots) & 1, lim);
+      for (int i = max(0, x_issued - Cfg::kXSlots); i < x_issued; ++i)
+        mbar_wait(&x_full[i % Cfg::kXSlots], (i / Cfg::kXSlots) & 1, lim);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA -----
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16<E>(kW4MmaRows, T);
+      const uint64_t desc0 = smem_desc_k_sw128(smem_u32(x_mem));
+      RingPos<Cfg::kXSlots> xp;
+      RingPos<Cfg::kASlots> as;
+      bool ok = true;
+      for (int i = 0; i < nk; ++i) {
+        ok = mbar_wait(&x_full[xp.idx], xp.phase, lim) && mbar_wait(&a_full[as.idx], as.phase, lim);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t desc = desc0 + ((xp.idx * Cfg::kXSlot) >> 4);
+        const uint32_t a_col = a_col0 + as.idx * Cfg::kACols;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)             // 16 columns each: 8 TMEM columns, 32 bytes of x
+          mma_f16_tmem_a(acc_col, a_col + k * 8,
+                         desc + (((k >> 2) * Cfg::kXBox + (k & 3) * 32) >> 4), idesc,
+                         i == 0 && k == 0 ? 0u : 1u);
+        mma_commit(&x_empty[xp.idx]);
+        mma_commit(&a_empty[as.idx]);
+        xp.next();
+        as.next();
+      }
+      if (!ok) record_status(a.status, kStatusTimeout, 1);
+      // all issued MMAs finish before the sums are read or TMEM is released
+      mma_commit(&acc_full);
+      mbar_wait(&acc_full, 0, lim);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // --------------------------------------------------------- unpack -----
+    const int q = warp & 3, row = q * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const int n_row = strip0 * 16 + row;        // of the layer
+    const bool in = n_row < a.N[l];
+    const unsigned short* sp = reinterpret_cast<const unsigned short*>(a.ws[l]) +
+                               static_cast<size_t>(in ? n_row : 0) * a.G;
+    // the scales of the four words' groups of a tile; one behind K is zero
+    auto scales = [&](int kb, uint32_t (&s)[4]) {
+      s[0] = s[1] = s[2] = s[3] = 0;
+      if (!in || kb >= a.kbs) return;
+      const int k = kb * 128;
+      s[0] = __ldg(sp + (k >> a.gs_shift));
+      if (a.gs_shift >= 7) {
+        s[1] = s[2] = s[3] = s[0];
+      } else {
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+          if (k + 32 * j < a.K) s[j] = __ldg(sp + ((k + 32 * j) >> a.gs_shift));
+      }
+    };
+    uint32_t s_cur[4], s_next[4];
+    scales(kb0, s_cur);
+    RingPos<Cfg::kWSlots> wp;
+    RingPos<Cfg::kASlots> as;
+    bool ok = true;
+    for (int i = 0; i < nk; ++i) {
+      scales(i + 1 < nk ? kb0 + i + 1 : a.kbs, s_next);
+      ok = warp_wait(&w_full[wp.idx], wp.phase, lim);
+      if (!ok) break;
+      // chunk t of the row lies at t ^ (row / 2 % 4): the box's 64-byte swizzle
+      const uint4* src = reinterpret_cast<const uint4*>(w_mem + wp.idx * kW4MmaTileBytes + row * 64);
+      uint4 c[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) c[t] = src[t ^ ((row >> 1) & 3)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_empty[wp.idx]);
+      ok = warp_wait(&a_empty[as.idx], as.phase ^ 1u, lim);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t col = lane_base + a_col0 + as.idx * Cfg::kACols;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // words 2h and 2h + 1: columns 64 h .. +63, chunk t's eight at 32 j + 8 t
+        uint32_t out[32];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const RowScale<E> s(s_cur[2 * h + j]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            s.apply(reinterpret_cast<const uint32_t*>(&c[t])[2 * h + j], out + 16 * j + 4 * t);
+        }
+        tmem_st32(col + 32 * h, out);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[as.idx]);
+      wp.next();
+      as.next();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s_cur[j] = s_next[j];
+    }
+    // ------------------------------------------------------- epilogue -----
+    if (ok) ok = warp_wait(&acc_full, 0, lim);
+    if (!ok && lane == 0) record_status(a.status, kStatusTimeout, 2);
+    if (ok) {
+      tc_fence_after();
+      E* y = static_cast<E*>(a.y[l]) + n_row;
+      float* sums = reinterpret_cast<float*>(base);     // [T][128], for the cluster
+#pragma unroll 1
+      for (int c0 = 0; c0 < T; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(lane_base + acc_col + c0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int m = mt * T + c0 + j;
+          if (a.split > 1)
+            sums[(c0 + j) * kW4MmaRows + row] = __uint_as_float(v[j]);
+          else if (in && m < a.M)
+            y[m * a.ldy[l]] = Elem<E>::from_float(__uint_as_float(v[j]));
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown --
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+  if (a.split > 1) {
+    cluster_sync_all();
+    // every rank adds up the ranks' sums for its share of the tokens
+    const int t0 = rank * T / a.split, t1 = (rank + 1) * T / a.split;
+    for (int i = t0 * kW4MmaRows + threadIdx.x; i < t1 * kW4MmaRows; i += kW4MmaThreads) {
+      const int m = mt * T + i / kW4MmaRows, n = strip0 * 16 + i % kW4MmaRows;
+      const uint32_t at = smem_u32(base) + static_cast<uint32_t>(i) * 4;
+      float v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        v[r] = 0.0f;
+        if (r < a.split)
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(map_to_rank(at, r)) : "memory");
+      }
+      float sum = v[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) sum += v[r];
+      if (m < a.M && n < a.N[l]) static_cast<E*>(a.y[l])[m * a.ldy[l] + n] = Elem<E>::from_float(sum);
+    }
+    cluster_sync_all();                 // no CTA leaves while another reads its sums
+  }
+}
+
+}  // namespace flexq

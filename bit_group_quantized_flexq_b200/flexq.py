@@ -8,6 +8,7 @@ raised.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -121,7 +122,7 @@ def lib():
             "flexq_linear_w4": (c_int, [c_int, c_int, c_int, c_int, c_int, c_void_p, c_ll,
                                         c_void_p, c_void_p, c_void_p, c_ll, c_void_p]),
             "flexq_linear_w4_group": (c_int, [c_int, c_int, c_int, c_int, c_void_p, c_ll, c_int,
-                                              ctypes.POINTER(Layer4), c_void_p]),
+                                              c_void_p, c_void_p]),
             "flexq_embedding": (c_int, [c_ll, c_int, c_int, c_int, c_int, c_int, c_void_p, c_int,
                                         c_void_p, c_void_p, ctypes.c_float, c_void_p, c_void_p]),
             "flexq_embedding_backward_workspace_bytes": (c_size_t, [c_ll, c_int]),
@@ -498,6 +499,7 @@ def linear_group(x, weights, group_size, act_bits=6, outs=None, workspace_buf=No
 # checked in one expression each, and taken apart (_need, _need_rows) only to
 # word a refusal.
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_LAYER4 = struct.Struct("@i4xPPPq").pack     # flexq_layer4_t
 
 
 def _is(t, dtype, shape, dev):
@@ -599,7 +601,7 @@ def _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out):
     if not _is(ws, torch.float16, (N, K // group_size), dev):
         _refuse(ws, "ws", torch.float16, (N, K // group_size), x)
     if out is None:
-        return torch.empty((M, N), dtype=dtype, device=x.device), N
+        return x.new_empty((M, N)), N
     if not _is_rows(out, dtype, (M, N), dev):
         _refuse_rows(out, "out", dtype, (M, N), x)
     return out, _row_stride(out, M, N)
@@ -635,15 +637,14 @@ def linear4_group(x, weights, group_size, outs=None):
         raise ValueError(f"1..{MAX_GROUP_LAYERS} layers, got {len(weights)}")
     if outs is not None and len(outs) != len(weights):
         raise ValueError(f"{len(weights)} layers, {len(outs)} outputs")
-    arr = (Layer4 * len(weights))()
-    ys = []
+    layers, ys = b"", []
     for i, (wp, ws, N) in enumerate(weights):
         y, ldy = _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev,
                            None if outs is None else outs[i])
-        arr[i] = (N, wp.data_ptr(), ws.data_ptr(), y.data_ptr(), ldy)
+        layers += _LAYER4(N, wp.data_ptr(), ws.data_ptr(), y.data_ptr(), ldy)
         ys.append(y)
     _launch(dev, lib().flexq_linear_w4_group, M, K, group_size, _DTYPES[dtype], x.data_ptr(), ldx,
-            len(weights), arr)
+            len(weights), layers)
     return ys
 
 
@@ -691,7 +692,7 @@ def embedding(ids, wp, ws, V, group_size, scale=1.0, weight_bits=4, dtype=torch.
     if not _is(ws, torch.float16, _scales_shape(V, K, group_size, weight_bits), dev):
         _refuse(ws, "ws", torch.float16, _scales_shape(V, K, group_size, weight_bits), ids)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=ids.device)
+        out = ws.new_empty(shape, dtype=dtype)
     elif not _is(out, dtype, shape, dev):
         _refuse(out, "out", dtype, shape, ids)
     _launch(dev, lib().flexq_embedding, ids.numel(), V, K, group_size, weight_bits, _DTYPES[dtype],

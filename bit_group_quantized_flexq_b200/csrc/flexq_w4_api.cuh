@@ -105,13 +105,13 @@ int encode_w4_x_map(CUtensorMap* map, const void* x, int dtype, int M, int K, lo
 }
 
 // The packed form as strips of 16 kbs rows of 64 bytes; box = one tile of 128
-// columns of eight strips, 64-byte swizzle.  Strips past the last read as zero.
-int encode_w4_map(CUtensorMap* map, const void* wp, int N, int kbs) {
+// columns of some strips, 64-byte swizzle.  Strips past the last read as zero.
+int encode_w4_map(CUtensorMap* map, const void* wp, int N, int kbs, int strips) {
   auto fn = encode_fn();
   if (!fn) return fail(FLEXQ_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[3] = {16u, static_cast<cuuint64_t>(kbs) * 16, static_cast<cuuint64_t>(flexq::w4_row_tiles(N))};
   cuuint64_t strides[2] = {64u, static_cast<cuuint64_t>(kbs) * flexq::kW4TileBytes};
-  cuuint32_t box[3] = {16u, 16u, 8u};
+  cuuint32_t box[3] = {16u, 16u, static_cast<cuuint32_t>(strips)};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(wp), dims, strides,
                         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
@@ -121,73 +121,48 @@ int encode_w4_map(CUtensorMap* map, const void* wp, int N, int kbs) {
   return FLEXQ_OK;
 }
 
-cudaLaunchConfig_t w4_mma_config(int smem, long long ctas, int split, cudaLaunchAttribute (&attr)[2],
-                                 cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(flexq::kW4MmaThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  return cfg;
+// CTAs of a cluster that share a tile's columns: as many as still run in one
+// wave (a sixteenth of the machine's places is left, as clusters do not fill
+// every group of SMs), each with at least four column tiles.
+int w4_mma_split(long long tiles, int kbs, long long slots) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= slots * 15 / 16 && kbs >= 8 * split) split *= 2;
+  return split;
 }
 
-// How many clusters of `split` CTAs run at once (asked once per device).
-template <typename E, int T>
-int w4_mma_clusters(int split, int* clusters) {
-  static int known[kMaxDevices][9];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  {
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
-    *clusters = known[dev][split];
-  }
-  if (*clusters > 0) return FLEXQ_OK;
-  cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = w4_mma_config(flexq::W4MmaCfg<T>::kSmem, split, split, attr, nullptr);
-  cfg.attrs = attr + 1;
-  cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(clusters, flexq::w4_mma_kernel<E, T>, &cfg);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
-  *clusters = std::max(1, *clusters);
-  std::lock_guard<std::mutex> lock(g_dev_mutex);
-  known[dev][split] = *clusters;
-  return FLEXQ_OK;
-}
-
-template <typename E, int T>
+template <typename E, int T, int RB>
 int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, long long ldx, int sms,
                   cudaStream_t stream) {
+  using Cfg = flexq::W4MmaCfg<T, RB>;
   constexpr int dtype = std::is_same<E, __half>::value ? FLEXQ_DTYPE_FP16 : FLEXQ_DTYPE_BF16;
   static bool ready[kMaxDevices];
-  cudaError_t e = allow_smem(flexq::w4_mma_kernel<E, T>, flexq::W4MmaCfg<T>::kSmem, ready);
+  cudaError_t e = allow_smem(flexq::w4_mma_kernel<E, T, RB>, Cfg::kSmem, ready);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   int rc = encode_w4_x_map(&a.x, x, dtype, a.M, a.K, ldx, T);
-  for (int l = 0; !rc && l < L.n; ++l) rc = encode_w4_map(&a.w[l], L.wp[l], L.N[l], a.kbs);
+  for (int l = 0; !rc && l < L.n; ++l) {
+    rc = encode_w4_map(&a.w[l], L.wp[l], L.N[l], a.kbs, 8 * RB);
+    a.tile0[l + 1] = a.tile0[l] + (L.N[l] + Cfg::kRows - 1) / Cfg::kRows;
+  }
   if (rc) return rc;
   a.token_tiles = (a.M + T - 1) / T;
   const long long tiles = static_cast<long long>(a.tile0[L.n]) * a.token_tiles;
-  // a tile's columns are shared by as many CTAs as still run in one wave, each
-  // with at least four column tiles
-  a.split = 1;
-  for (int s = 2; s <= 8 && tiles * s <= 2LL * sms && a.kbs >= 4 * s; s *= 2) {
-    int clusters = 0;
-    if ((rc = w4_mma_clusters<E, T>(s, &clusters))) return rc;
-    if (tiles > clusters) break;
-    a.split = s;
-  }
-  if (tiles * a.split > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d with %d weight rows too large", a.M, a.tile0[L.n] * 128);
+  a.split = w4_mma_split(tiles, a.kbs, static_cast<long long>(Cfg::kCtasPerSm) * sms);
+  if (tiles * a.split > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d with so many weight rows is too large", a.M);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = w4_mma_config(flexq::W4MmaCfg<T>::kSmem, tiles * a.split, a.split, attr, stream);
-  e = cudaLaunchKernelEx(&cfg, flexq::w4_mma_kernel<E, T>, a);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, flexq::w4_mma_kernel<E, T, RB>, a);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
   return FLEXQ_OK;
 }
@@ -206,7 +181,6 @@ int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, i
     m.y[l] = L.y[l];
     m.ldy[l] = L.ldy[l];
     m.N[l] = L.N[l];
-    m.tile0[l + 1] = m.tile0[l] + (L.N[l] + flexq::kW4MmaRows - 1) / flexq::kW4MmaRows;
   }
   m.M = a.M;
   m.K = a.K;
@@ -215,10 +189,11 @@ int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, i
   m.gs_shift = a.gs_shift;
   m.status = a.status;
   m.wait_limit_ns = a.wait_limit_ns;
-  return a.M <= 16   ? launch_w4_mma<E, 16>(m, L, a.x, a.ldx, sms, s)
-         : a.M <= 32 ? launch_w4_mma<E, 32>(m, L, a.x, a.ldx, sms, s)
-         : a.M <= 64 ? launch_w4_mma<E, 64>(m, L, a.x, a.ldx, sms, s)
-                     : launch_w4_mma<E, 128>(m, L, a.x, a.ldx, sms, s);
+  return a.M <= 16    ? launch_w4_mma<E, 16, 1>(m, L, a.x, a.ldx, sms, s)
+         : a.M <= 32  ? launch_w4_mma<E, 32, 1>(m, L, a.x, a.ldx, sms, s)
+         : a.M <= 64  ? launch_w4_mma<E, 64, 1>(m, L, a.x, a.ldx, sms, s)
+         : a.M <= 256 ? launch_w4_mma<E, 128, 1>(m, L, a.x, a.ldx, sms, s)
+                      : launch_w4_mma<E, 128, 2>(m, L, a.x, a.ldx, sms, s);
 }
 
 int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long ldx, int n_layers,

@@ -1,12 +1,14 @@
 // flexq_w4_gemm.cuh -- 4-bit linear layers for batches beyond the streaming
 // kernel's, on the tensor core's tcgen05 MMA.
 //
-// One CTA: 128 weight rows x T tokens over its share of the columns.  The
-// weights are the MMA's A operand, in tensor memory: unpack warps turn a tile
+// One CTA: RB blocks of 128 weight rows x T tokens over its share of the
+// columns.  The weights are the MMA's A operand, in tensor memory: unpack warps turn a tile
 // of 128 rows x 128 columns (8 KB of codes, one TMA box) into FP16 or BF16
 // values and store them there; the activations are the B operand, in shared
-// memory as TMA brings them; one FP32 accumulator of T columns takes the whole
-// share.  An unpacked weight is the rounded product of code and scale, half a
+// memory as TMA brings them; one FP32 accumulator of T columns per row block takes the
+// whole share.  Two row blocks read each tile of activations once: with one, 128
+// tokens bring 32 KB from L2 for 512 cycles of MMA, more than an SM receives
+// in them.  An unpacked weight is the rounded product of code and scale, half a
 // step of the activations' type: keeping the codes whole and scaling each
 // group's sum instead would read the accumulator back once per group, which
 // costs a tile of 128 tokens more time than its MMAs.
@@ -35,6 +37,17 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u),
       "r"(0u), "r"(0u)
       : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 // Instruction descriptor: FP16 or BF16 operands, FP32 accumulator, both
@@ -90,39 +103,43 @@ struct RowScale<__nv_bfloat16> {
   }
 };
 
-constexpr int kW4MmaThreads = 256;      // warps 0 producer, 1 MMA, 2-3 idle, 4-7 unpack + epilogue
-constexpr int kW4MmaRows = 128;
-constexpr int kW4MmaTileBytes = 8 * kW4TileBytes;
-
-template <int T>
+template <int T, int RB>
 struct W4MmaCfg {
+  // Warps: 0 producer, 1 MMA, 2-3 idle, the others unpack and write the sums
+  // out, eight to a row block: two to a quarter of its rows with half a
+  // tile's columns each (with one, unpacking took longer than the MMAs).
+  static constexpr int kUnpackWarps = 8 * RB;
+  static constexpr int kThreads = 128 + 32 * kUnpackWarps;
+  static constexpr int kCtasPerSm = 2 / RB;
+  static constexpr int kRows = 128 * RB;
   static constexpr int kXBox = T * 128;                 // 64 columns of T tokens
   static constexpr int kXSlot = 2 * kXBox;
-  static constexpr int kXSlots = T == 128 ? 2 : T == 64 ? 4 : T == 32 ? 6 : 8;
+  static constexpr int kXSlots = RB == 2 ? 4 : T == 128 ? 2 : T == 64 ? 4 : T == 32 ? 6 : 8;
+  static constexpr int kWSlot = 8 * RB * kW4TileBytes;  // 128 columns of the rows
   static constexpr int kWSlots = T == 128 ? 4 : T == 16 ? 6 : 5;
   static constexpr int kXBytes = kXSlots * kXSlot;
-  static constexpr int kWBytes = kWSlots * kW4MmaTileBytes;
+  static constexpr int kWBytes = kWSlots * kWSlot;
   // the sums a CTA leaves for its cluster lie over the operand slots
-  static constexpr int kMain = kXBytes + kWBytes > T * kW4MmaRows * 4 ? kXBytes + kWBytes
-                                                                     : T * kW4MmaRows * 4;
+  static constexpr int kMain = kXBytes + kWBytes > T * kRows * 4 ? kXBytes + kWBytes : T * kRows * 4;
   static constexpr int kSmem = kMain + 1024;            // aligned to the swizzle's 1024 bytes
   static constexpr int kAccCols = T < 32 ? 32 : T;
   static constexpr int kACols = 64;                     // 128 columns of weights
   static constexpr int kASlots = 2;
-  static constexpr int kTmemCols = 256;                 // two CTAs share an SM's 512
-  static_assert(kAccCols + kASlots * kACols <= kTmemCols, "tensor memory");
-  // a third CTA on the SM would wait for tensor memory
-  static_assert(3 * kSmem > 227 * 1024 && 2 * (kSmem + 2048) <= 228 * 1024, "two CTAs per SM");
+  static constexpr int kTmemCols = 256 * RB;            // of an SM's 512
+  static_assert(RB * (kAccCols + kASlots * kACols) <= kTmemCols, "tensor memory");
+  // one CTA more on the SM would wait for tensor memory
+  static_assert((kCtasPerSm + 1) * kSmem > 227 * 1024 && kCtasPerSm * (kSmem + 2048) <= 228 * 1024,
+                "CTAs per SM");
 };
 
 struct W4MmaArgs {
   CUtensorMap x;                        // [M][K], boxes of 64 columns x T tokens, 128-byte swizzle
-  CUtensorMap w[kW4MaxLayers];          // [strip][16 kbs rows][64 bytes], boxes of 8 strips, 64-byte swizzle
+  CUtensorMap w[kW4MaxLayers];          // [strip][16 kbs rows][64 bytes], boxes of 8 RB strips, 64-byte swizzle
   const __half* ws[kW4MaxLayers];
   void* y[kW4MaxLayers];
   long long ldy[kW4MaxLayers];
   int N[kW4MaxLayers];
-  int tile0[kW4MaxLayers + 1];          // first tile of 128 rows of each layer
+  int tile0[kW4MaxLayers + 1];          // first tile of 128 RB rows of each layer
   int n;
   int M, K, G, kbs, gs_shift;
   int split;                            // CTAs of a cluster, which share a tile's columns
@@ -131,9 +148,10 @@ struct W4MmaArgs {
   unsigned long long wait_limit_ns;
 };
 
-template <typename E, int T>
-__global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_constant__ W4MmaArgs a) {
-  using Cfg = W4MmaCfg<T>;
+template <typename E, int T, int RB>
+__global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kCtasPerSm)
+    w4_mma_kernel(const __grid_constant__ W4MmaArgs a) {
+  using Cfg = W4MmaCfg<T, RB>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t x_full[Cfg::kXSlots], x_empty[Cfg::kXSlots];
   __shared__ uint64_t w_full[Cfg::kWSlots], w_empty[Cfg::kWSlots];
@@ -151,7 +169,7 @@ __global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_c
   const int mt = tile % a.token_tiles, rt = tile / a.token_tiles;
   int l = 0;
   while (l + 1 < a.n && rt >= a.tile0[l + 1]) ++l;
-  const int strip0 = (rt - a.tile0[l]) * 8;
+  const int strip0 = (rt - a.tile0[l]) * 8 * RB;
   const int kb0 = static_cast<int>(static_cast<long long>(rank) * a.kbs / a.split);
   const int nk = static_cast<int>(static_cast<long long>(rank + 1) * a.kbs / a.split) - kb0;
 
@@ -162,10 +180,10 @@ __global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_c
     }
     for (int i = 0; i < Cfg::kWSlots; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 4);
+      mbar_init(&w_empty[i], Cfg::kUnpackWarps);
     }
     for (int i = 0; i < Cfg::kASlots; ++i) {
-      mbar_init(&a_full[i], 4);
+      mbar_init(&a_full[i], Cfg::kUnpackWarps);
       mbar_init(&a_empty[i], 1);
     }
     mbar_init(&acc_full, 1);
@@ -173,8 +191,8 @@ __global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_c
   }
   auto load_w = [&](int i) {
     uint64_t* bar = &w_full[i % Cfg::kWSlots];
-    mbar_arrive_expect_tx(bar, kW4MmaTileBytes);
-    tma_load_3d(w_mem + i % Cfg::kWSlots * kW4MmaTileBytes, &a.w[l], bar, 0, (kb0 + i) * 16, strip0);
+    mbar_arrive_expect_tx(bar, Cfg::kWSlot);
+    tma_load_3d(w_mem + i % Cfg::kWSlots * Cfg::kWSlot, &a.w[l], bar, 0, (kb0 + i) * 16, strip0);
   };
   auto load_x = [&](int i) {
     uint64_t* bar = &x_full[i % Cfg::kXSlots];
@@ -190,7 +208,7 @@ __global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
-  const uint32_t acc_col = tmem, a_col0 = tmem + Cfg::kAccCols;
+  const uint32_t acc_col = tmem, a_col0 = tmem + RB * Cfg::kAccCols;
   grid_launch_dependents();
 
   if (warp == 0) {
@@ -226,97 +244,93 @@ __global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_c
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA -----
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16<E>(kW4MmaRows, T);
-      const uint64_t desc0 = smem_desc_k_sw128(smem_u32(x_mem));
-      RingPos<Cfg::kXSlots> xp;
-      RingPos<Cfg::kASlots> as;
-      bool ok = true;
-      for (int i = 0; i < nk; ++i) {
-        ok = mbar_wait(&x_full[xp.idx], xp.phase, lim) && mbar_wait(&a_full[as.idx], as.phase, lim);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t desc = desc0 + ((xp.idx * Cfg::kXSlot) >> 4);
-        const uint32_t a_col = a_col0 + as.idx * Cfg::kACols;
+    // The whole warp waits and one elected lane issues, so that the compiler
+    // knows the operands to be uniform.
+    constexpr uint32_t idesc = idesc_f16<E>(128, T);
+    const uint64_t desc0 = smem_desc_k_sw128(smem_u32(x_mem));
+    RingPos<Cfg::kXSlots> xp;
+    RingPos<Cfg::kASlots> as;
+    bool ok = true;
+    for (int i = 0; i < nk; ++i) {
+      ok = warp_wait(&x_full[xp.idx], xp.phase, lim) && warp_wait(&a_full[as.idx], as.phase, lim);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t desc = desc0 + ((xp.idx * Cfg::kXSlot) >> 4);
+      const uint32_t a_col = a_col0 + as.idx * (RB * Cfg::kACols);
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)             // 16 columns each: 8 TMEM columns, 32 bytes of x
-          mma_f16_tmem_a(acc_col, a_col + k * 8,
-                         desc + (((k >> 2) * Cfg::kXBox + (k & 3) * 32) >> 4), idesc,
-                         i == 0 && k == 0 ? 0u : 1u);
+        for (int k = 0; k < 8 * RB; ++k)        // 16 columns each: 8 TMEM columns, 32 bytes of x
+          mma_f16_tmem_a(acc_col + k / 8 * Cfg::kAccCols, a_col + k * 8,
+                         desc + (((k >> 2 & 1) * Cfg::kXBox + (k & 3) * 32) >> 4), idesc,
+                         i == 0 && k % 8 == 0 ? 0u : 1u);
         mma_commit(&x_empty[xp.idx]);
         mma_commit(&a_empty[as.idx]);
-        xp.next();
-        as.next();
       }
-      if (!ok) record_status(a.status, kStatusTimeout, 1);
-      // all issued MMAs finish before the sums are read or TMEM is released
-      mma_commit(&acc_full);
-      mbar_wait(&acc_full, 0, lim);
+      __syncwarp();
+      xp.next();
+      as.next();
     }
-    __syncwarp();
+    if (!ok && lane == 0) record_status(a.status, kStatusTimeout, 1);
+    // all issued MMAs finish before the sums are read or TMEM is released
+    if (elect_one()) mma_commit(&acc_full);
+    warp_wait(&acc_full, 0, lim);
   } else if (warp >= 4) {
     // --------------------------------------------------------- unpack -----
-    const int q = warp & 3, row = q * 32 + lane;
+    const int q = warp & 3, h = (warp - 4) >> 2 & 1, rb = (warp - 4) >> 3;
+    const int row = rb * 128 + q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const int n_row = strip0 * 16 + row;        // of the layer
     const bool in = n_row < a.N[l];
     const unsigned short* sp = reinterpret_cast<const unsigned short*>(a.ws[l]) +
                                static_cast<size_t>(in ? n_row : 0) * a.G;
-    // the scales of the four words' groups of a tile; one behind K is zero
-    auto scales = [&](int kb, uint32_t (&s)[4]) {
-      s[0] = s[1] = s[2] = s[3] = 0;
-      if (!in || kb >= a.kbs) return;
-      const int k = kb * 128;
-      s[0] = __ldg(sp + (k >> a.gs_shift));
-      if (a.gs_shift >= 7) {
-        s[1] = s[2] = s[3] = s[0];
-      } else {
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-          if (k + 32 * j < a.K) s[j] = __ldg(sp + ((k + 32 * j) >> a.gs_shift));
-      }
+    // the scales of the groups of words 2 h and 2 h + 1 of tile i; one behind
+    // the last row or column is zero
+    auto scales = [&](int i, uint32_t (&s)[2]) {
+      const int k = (kb0 + i) * 128 + h * 64;
+      s[0] = s[1] = 0;
+      if (!in || i >= nk) return;
+      if (k < a.K) s[0] = __ldg(sp + (k >> a.gs_shift));
+      if (a.gs_shift >= 6) s[1] = s[0];
+      else if (k + 32 < a.K) s[1] = __ldg(sp + ((k + 32) >> a.gs_shift));
     };
-    uint32_t s_cur[4], s_next[4];
-    scales(kb0, s_cur);
     RingPos<Cfg::kWSlots> wp;
-    RingPos<Cfg::kASlots> as;
-    bool ok = true;
-    for (int i = 0; i < nk; ++i) {
-      scales(i + 1 < nk ? kb0 + i + 1 : a.kbs, s_next);
-      ok = warp_wait(&w_full[wp.idx], wp.phase, lim);
-      if (!ok) break;
+    uint32_t phase = 1;                         // of the A slots' release
+    auto unpack = [&](int i, int slot, uint32_t (&s)[2]) -> bool {
+      if (!warp_wait(&w_full[wp.idx], wp.phase, lim)) return false;
       // chunk t of the row lies at t ^ (row / 2 % 4): the box's 64-byte swizzle
-      const uint4* src = reinterpret_cast<const uint4*>(w_mem + wp.idx * kW4MmaTileBytes + row * 64);
-      uint4 c[4];
+      const uint2* src = reinterpret_cast<const uint2*>(w_mem + wp.idx * Cfg::kWSlot + row * 64) + h;
+      uint2 c[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) c[t] = src[t ^ ((row >> 1) & 3)];
+      for (int t = 0; t < 4; ++t) c[t] = src[(t ^ ((row >> 1) & 3)) * 2];
       __syncwarp();
       if (lane == 0) mbar_arrive(&w_empty[wp.idx]);
-      ok = warp_wait(&a_empty[as.idx], as.phase ^ 1u, lim);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t col = lane_base + a_col0 + as.idx * Cfg::kACols;
+      wp.next();
+      // columns 64 h .. +63; chunk t's eight of word j at 32 j + 8 t
+      uint32_t out[32];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // words 2h and 2h + 1: columns 64 h .. +63, chunk t's eight at 32 j + 8 t
-        uint32_t out[32];
+      for (int j = 0; j < 2; ++j) {
+        const RowScale<E> scale(s[j]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const RowScale<E> s(s_cur[2 * h + j]);
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            s.apply(reinterpret_cast<const uint32_t*>(&c[t])[2 * h + j], out + 16 * j + 4 * t);
-        }
-        tmem_st32(col + 32 * h, out);
+        for (int t = 0; t < 4; ++t) scale.apply(j == 0 ? c[t].x : c[t].y, out + 16 * j + 4 * t);
       }
+      scales(i + Cfg::kASlots, s);              // for this slot's next tile
+      if (!warp_wait(&a_empty[slot], phase, lim)) return false;
+      tc_fence_after();
+      tmem_st32(lane_base + a_col0 + (slot * RB + rb) * Cfg::kACols + 32 * h, out);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&a_full[as.idx]);
-      wp.next();
-      as.next();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s_cur[j] = s_next[j];
+      if (lane == 0) mbar_arrive(&a_full[slot]);
+      return true;
+    };
+    uint32_t s0[2], s1[2];
+    scales(0, s0);
+    scales(1, s1);
+    bool ok = true;
+    static_assert(Cfg::kASlots == 2, "the loop below takes two tiles at a time");
+    for (int i = 0; ok && i < nk; i += 2, phase ^= 1) {
+      ok = unpack(i, 0, s0);
+      if (ok && i + 1 < nk) ok = unpack(i + 1, 1, s1);
     }
     // ------------------------------------------------------- epilogue -----
     if (ok) ok = warp_wait(&acc_full, 0, lim);
@@ -324,17 +338,17 @@ __global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_c
     if (ok) {
       tc_fence_after();
       E* y = static_cast<E*>(a.y[l]) + n_row;
-      float* sums = reinterpret_cast<float*>(base);     // [T][128], for the cluster
+      float* sums = reinterpret_cast<float*>(base);     // [T][rows], for the cluster
 #pragma unroll 1
-      for (int c0 = 0; c0 < T; c0 += 16) {
+      for (int c0 = 16 * h; c0 < T; c0 += 32) {         // the two warps of a quarter take turns
         uint32_t v[16];
-        tmem_ld16(lane_base + acc_col + c0, v);
+        tmem_ld16(lane_base + acc_col + rb * Cfg::kAccCols + c0, v);
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int m = mt * T + c0 + j;
           if (a.split > 1)
-            sums[(c0 + j) * kW4MmaRows + row] = __uint_as_float(v[j]);
+            sums[(c0 + j) * Cfg::kRows + row] = __uint_as_float(v[j]);
           else if (in && m < a.M)
             y[m * a.ldy[l]] = Elem<E>::from_float(__uint_as_float(v[j]));
         }
@@ -353,8 +367,8 @@ __global__ void __launch_bounds__(kW4MmaThreads, 2) w4_mma_kernel(const __grid_c
     cluster_sync_all();
     // every rank adds up the ranks' sums for its share of the tokens
     const int t0 = rank * T / a.split, t1 = (rank + 1) * T / a.split;
-    for (int i = t0 * kW4MmaRows + threadIdx.x; i < t1 * kW4MmaRows; i += kW4MmaThreads) {
-      const int m = mt * T + i / kW4MmaRows, n = strip0 * 16 + i % kW4MmaRows;
+    for (int i = t0 * Cfg::kRows + threadIdx.x; i < t1 * Cfg::kRows; i += Cfg::kThreads) {
+      const int m = mt * T + i / Cfg::kRows, n = strip0 * 16 + i % Cfg::kRows;
       const uint32_t at = smem_u32(base) + static_cast<uint32_t>(i) * 4;
       float v[8];
 #pragma unroll

@@ -50,6 +50,25 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// 16 lanes x 256 bits twice along the columns (16 columns): thread t gets lane
+// t/4, columns 8i + 2(t%4) and the one behind, and the same of lane t/4 + 8,
+// in r[4i .. 4i+3] for i = 0, 1.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values, each stored transposed: lane 8 b + i
+// gives the address of the eight values that were column i of block b.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&p)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+               : "memory");
+}
+
 // Instruction descriptor: FP16 or BF16 operands, FP32 accumulator, both
 // K-major, M x N.
 template <typename T>
@@ -119,7 +138,9 @@ struct W4MmaCfg {
   static constexpr int kWSlots = T == 128 ? 4 : T == 16 ? 6 : 5;
   static constexpr int kXBytes = kXSlots * kXSlot;
   static constexpr int kWBytes = kWSlots * kWSlot;
-  // the sums a CTA leaves for its cluster lie over the operand slots
+  // results lie over the operand slots before they leave, or FP32 sums for
+  // the cluster; a token's results start half a bank line after the last one's
+  static constexpr int kOutPitch = kRows * 2 + 16;
   static constexpr int kMain = kXBytes + kWBytes > T * kRows * 4 ? kXBytes + kWBytes : T * kRows * 4;
   static constexpr int kSmem = kMain + 1024;            // aligned to the swizzle's 1024 bytes
   static constexpr int kAccCols = T < 32 ? 32 : T;
@@ -155,8 +176,8 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t x_full[Cfg::kXSlots], x_empty[Cfg::kXSlots];
   __shared__ uint64_t w_full[Cfg::kWSlots], w_empty[Cfg::kWSlots];
-  __shared__ uint64_t a_full[Cfg::kASlots], a_empty[Cfg::kASlots];
-  __shared__ uint64_t acc_full;
+  __shared__ uint64_t a_full[RB][Cfg::kASlots], a_empty[RB][Cfg::kASlots];
+  __shared__ uint64_t acc_full[RB];
   __shared__ uint32_t tmem_at;
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* x_mem = base;
@@ -176,17 +197,19 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < Cfg::kXSlots; ++i) {
       mbar_init(&x_full[i], 1);
-      mbar_init(&x_empty[i], 1);
+      mbar_init(&x_empty[i], RB);
     }
     for (int i = 0; i < Cfg::kWSlots; ++i) {
       mbar_init(&w_full[i], 1);
       mbar_init(&w_empty[i], Cfg::kUnpackWarps);
     }
-    for (int i = 0; i < Cfg::kASlots; ++i) {
-      mbar_init(&a_full[i], Cfg::kUnpackWarps);
-      mbar_init(&a_empty[i], 1);
+    for (int rb = 0; rb < RB; ++rb) {
+      for (int i = 0; i < Cfg::kASlots; ++i) {
+        mbar_init(&a_full[rb][i], 8);
+        mbar_init(&a_empty[rb][i], 1);
+      }
+      mbar_init(&acc_full[rb], 1);
     }
-    mbar_init(&acc_full, 1);
     fence_barrier_init();
   }
   auto load_w = [&](int i) {
@@ -242,29 +265,31 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
         mbar_wait(&x_full[i % Cfg::kXSlots], (i / Cfg::kXSlots) & 1, lim);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= RB) {
     // ------------------------------------------------------------ MMA -----
-    // The whole warp waits and one elected lane issues, so that the compiler
-    // knows the operands to be uniform.
+    // A warp per row block: while one waits at its barriers the other's MMAs
+    // run.  The whole warp waits and one elected lane issues, so that the
+    // compiler knows the operands to be uniform.
+    const int rb = warp - 1;
     constexpr uint32_t idesc = idesc_f16<E>(128, T);
     const uint64_t desc0 = smem_desc_k_sw128(smem_u32(x_mem));
+    const uint32_t acc = acc_col + rb * Cfg::kAccCols;
     RingPos<Cfg::kXSlots> xp;
     RingPos<Cfg::kASlots> as;
     bool ok = true;
     for (int i = 0; i < nk; ++i) {
-      ok = warp_wait(&x_full[xp.idx], xp.phase, lim) && warp_wait(&a_full[as.idx], as.phase, lim);
+      ok = warp_wait(&x_full[xp.idx], xp.phase, lim) && warp_wait(&a_full[rb][as.idx], as.phase, lim);
       if (!ok) break;
       tc_fence_after();
       const uint64_t desc = desc0 + ((xp.idx * Cfg::kXSlot) >> 4);
-      const uint32_t a_col = a_col0 + as.idx * (RB * Cfg::kACols);
+      const uint32_t a_col = a_col0 + (as.idx * RB + rb) * Cfg::kACols;
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8 * RB; ++k)        // 16 columns each: 8 TMEM columns, 32 bytes of x
-          mma_f16_tmem_a(acc_col + k / 8 * Cfg::kAccCols, a_col + k * 8,
-                         desc + (((k >> 2 & 1) * Cfg::kXBox + (k & 3) * 32) >> 4), idesc,
-                         i == 0 && k % 8 == 0 ? 0u : 1u);
+        for (int k = 0; k < 8; ++k)             // 16 columns each: 8 TMEM columns, 32 bytes of x
+          mma_f16_tmem_a(acc, a_col + k * 8, desc + (((k >> 2) * Cfg::kXBox + (k & 3) * 32) >> 4),
+                         idesc, i == 0 && k == 0 ? 0u : 1u);
         mma_commit(&x_empty[xp.idx]);
-        mma_commit(&a_empty[as.idx]);
+        mma_commit(&a_empty[rb][as.idx]);
       }
       __syncwarp();
       xp.next();
@@ -272,8 +297,8 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
     }
     if (!ok && lane == 0) record_status(a.status, kStatusTimeout, 1);
     // all issued MMAs finish before the sums are read or TMEM is released
-    if (elect_one()) mma_commit(&acc_full);
-    warp_wait(&acc_full, 0, lim);
+    if (elect_one()) mma_commit(&acc_full[rb]);
+    warp_wait(&acc_full[rb], 0, lim);
   } else if (warp >= 4) {
     // --------------------------------------------------------- unpack -----
     const int q = warp & 3, h = (warp - 4) >> 2 & 1, rb = (warp - 4) >> 3;
@@ -314,13 +339,13 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
         for (int t = 0; t < 4; ++t) scale.apply(j == 0 ? c[t].x : c[t].y, out + 16 * j + 4 * t);
       }
       scales(i + Cfg::kASlots, s);              // for this slot's next tile
-      if (!warp_wait(&a_empty[slot], phase, lim)) return false;
+      if (!warp_wait(&a_empty[rb][slot], phase, lim)) return false;
       tc_fence_after();
       tmem_st32(lane_base + a_col0 + (slot * RB + rb) * Cfg::kACols + 32 * h, out);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&a_full[slot]);
+      if (lane == 0) mbar_arrive(&a_full[rb][slot]);
       return true;
     };
     uint32_t s0[2], s1[2];
@@ -333,24 +358,41 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
       if (ok && i + 1 < nk) ok = unpack(i + 1, 1, s1);
     }
     // ------------------------------------------------------- epilogue -----
-    if (ok) ok = warp_wait(&acc_full, 0, lim);
+    // The sums go to shared memory, over the operands: as results of the
+    // activations' type, token by token, or in FP32 for the cluster to add up.
+    // The other row block's MMAs may still read the operands there.
+    for (int r = 0; ok && r < RB; ++r) ok = warp_wait(&acc_full[r], 0, lim);
     if (!ok && lane == 0) record_status(a.status, kStatusTimeout, 2);
     if (ok) {
       tc_fence_after();
-      E* y = static_cast<E*>(a.y[l]) + n_row;
-      float* sums = reinterpret_cast<float*>(base);     // [T][rows], for the cluster
+      const uint32_t acc = lane_base + acc_col + rb * Cfg::kAccCols;
 #pragma unroll 1
       for (int c0 = 16 * h; c0 < T; c0 += 32) {         // the two warps of a quarter take turns
-        uint32_t v[16];
-        tmem_ld16(lane_base + acc_col + rb * Cfg::kAccCols + c0, v);
-        tmem_wait_ld();
+        if (a.split > 1) {
+          uint32_t v[16];
+          tmem_ld16(acc + c0, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int m = mt * T + c0 + j;
-          if (a.split > 1)
-            sums[(c0 + j) * Cfg::kRows + row] = __uint_as_float(v[j]);
-          else if (in && m < a.M)
-            y[m * a.ldy[l]] = Elem<E>::from_float(__uint_as_float(v[j]));
+          for (int j = 0; j < 16; ++j)
+            reinterpret_cast<float*>(base)[(c0 + j) * Cfg::kRows + row] = __uint_as_float(v[j]);
+        } else {
+          // thread t holds tokens 2 (t % 4) + {0, 1} (+ 8 for the second four) of
+          // rows t / 4 and t / 4 + 8: 8 x 8 blocks as stmatrix takes them
+          uint32_t v[2][8];
+          tmem_ld_16x256b_x2(acc + c0, v[0]);
+          tmem_ld_16x256b_x2(acc + c0 + (16u << 16), v[1]);
+          tmem_wait_ld();
+          // lane 8 b + i gives the place of token i of block b: rows 8 (b % 2), tokens 8 (b / 2)
+          const uint32_t at = smem_u32(base) + (c0 + (lane >> 4) * 8 + (lane & 7)) * Cfg::kOutPitch +
+                              (rb * 128 + q * 32 + (lane >> 3 & 1) * 8) * 2;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            uint32_t p[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              p[b] = Elem<E>::pack(__uint_as_float(v[r][2 * b]), __uint_as_float(v[r][2 * b + 1]));
+            stmatrix_x4_trans(at + r * 32, p);
+          }
         }
       }
     }
@@ -363,27 +405,55 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }
-  if (a.split > 1) {
-    cluster_sync_all();
-    // every rank adds up the ranks' sums for its share of the tokens
-    const int t0 = rank * T / a.split, t1 = (rank + 1) * T / a.split;
-    for (int i = t0 * Cfg::kRows + threadIdx.x; i < t1 * Cfg::kRows; i += Cfg::kThreads) {
-      const int m = mt * T + i / Cfg::kRows, n = strip0 * 16 + i % Cfg::kRows;
-      const uint32_t at = smem_u32(base) + static_cast<uint32_t>(i) * 4;
-      float v[8];
+  // results leave in pieces of eight rows (of the weights) of a token
+  E* const y = static_cast<E*>(a.y[l]);
+  const long long ldy = a.ldy[l];
+  const int n0 = strip0 * 16, N = a.N[l];
+  const bool wide = ((ldy * 2) | static_cast<long long>(reinterpret_cast<uintptr_t>(y))) % 16 == 0;
+  auto write = [&](int token, int piece, const uint4& v) {
+    const int m = mt * T + token, n = n0 + piece * 8;
+    if (m >= a.M || n >= N) return;
+    E* at = y + m * ldy + n;
+    if (wide && n + 8 <= N) {
+      *reinterpret_cast<uint4*>(at) = v;
+    } else {
+      const E* e = reinterpret_cast<const E*>(&v);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        v[r] = 0.0f;
-        if (r < a.split)
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(map_to_rank(at, r)) : "memory");
-      }
-      float sum = v[0];
-#pragma unroll
-      for (int r = 1; r < 8; ++r) sum += v[r];
-      if (m < a.M && n < a.N[l]) static_cast<E*>(a.y[l])[m * a.ldy[l] + n] = Elem<E>::from_float(sum);
+      for (int j = 0; j < 8; ++j)
+        if (n + j < N) at[j] = e[j];
     }
-    cluster_sync_all();                 // no CTA leaves while another reads its sums
+  };
+  constexpr int kPieces = Cfg::kRows / 8;
+  if (a.split == 1) {
+    for (int i = threadIdx.x; i < T * kPieces; i += Cfg::kThreads)
+      write(i / kPieces, i % kPieces,
+            *reinterpret_cast<const uint4*>(base + i / kPieces * Cfg::kOutPitch + i % kPieces * 16));
+    return;
   }
+  cluster_sync_all();
+  // every rank adds up the ranks' sums for its share of the tokens
+  const int t0 = rank * T / a.split, t1 = (rank + 1) * T / a.split;
+  for (int i = t0 * kPieces + threadIdx.x; i < t1 * kPieces; i += Cfg::kThreads) {
+    const uint32_t at = smem_u32(base) + static_cast<uint32_t>(i) * 32;
+    float sum[8] = {};
+    for (int r = 0; r < a.split; ++r) {
+      float v[8];
+      const uint32_t p = map_to_rank(at, r);
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(p) : "memory");
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "r"(p + 16) : "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    }
+    uint4 o;
+    o.x = Elem<E>::pack(sum[0], sum[1]);
+    o.y = Elem<E>::pack(sum[2], sum[3]);
+    o.z = Elem<E>::pack(sum[4], sum[5]);
+    o.w = Elem<E>::pack(sum[6], sum[7]);
+    write(i / kPieces, i % kPieces, o);
+  }
+  cluster_sync_all();                   // no CTA leaves while another reads its sums
 }
 
 }  // namespace flexq

@@ -226,22 +226,24 @@ struct W4Args {
   const void* x;
   long long ldx;
   int M, K, G, kbs, gs_shift;     // kbs: tiles of 128 columns; gs = 1 << gs_shift
+  int split;                      // streaming kernel: CTAs of a cluster
   unsigned int* status;           // device status word
   unsigned long long wait_limit_ns;
 };
 
-// The product for batches of up to 8 tokens streams the weights once, so it is
-// bound by HBM; every SM must keep tens of KB of loads in flight from its
+// The product for batches of up to 16 tokens streams the weights once, so it
+// is bound by HBM; every SM must keep tens of KB of loads in flight from its
 // first to its last cycle.  A strip's tiles are cut into chunks of four tiles
-// (16 rows x 512 columns, 4 KB, one bulk copy); the chunks of a run of strips
-// are divided evenly among the 32 warps of a cluster of two CTAs (a pair of
-// SMs), wherever strips begin or end: no warp waits for another before the
-// end.  A warp brings a chunk into a buffer of its own while it multiplies the
-// one before in registers; the activations lie in shared memory.  Codes are exact in FP16 and BF16; the tensor core adds a
-// group's products in FP32, and the group's sum times the scale is added in
-// FP32.  What a warp has of a strip that it shares with others goes to shared
-// memory and is added, in the order of the columns, by the warp that holds the
-// strip's first chunk.
+// (16 rows x 512 columns, 4 KB, one bulk copy).  A cluster of one to eight
+// CTAs, one per SM, takes a run of strips; each of its CTAs takes a share of
+// their columns, whose activations it keeps in shared memory, and divides its
+// chunks evenly among 16 warps, wherever strips begin or end: no warp waits
+// for another before the end.  A warp brings a chunk into a buffer of its own
+// while it multiplies the one before in registers.  Codes are exact in FP16
+// and BF16; the tensor core adds a group's products in FP32, and the group's
+// sum times the scale is added in FP32.  What a warp has of a strip that it
+// shares with others is added, in the order of the columns, by the warp that
+// holds the strip's first chunk, and so are the CTAs' sums of a strip.
 //
 // Taking a code apart has to cost little: at HBM's rate an SM has about 44
 // cycles per tile.  So the tensor core multiplies codes with an offset, u = q
@@ -250,9 +252,8 @@ struct W4Args {
 // which every CTA forms once while its first weights are on the way.
 constexpr int kGemvWarps = 16;
 constexpr int kGemvThreads = kGemvWarps * 32;
-constexpr int kGemvCluster = 2;
-constexpr int kGemvShares = kGemvWarps * kGemvCluster;
 constexpr int kGemvChunk = 4;                 // tiles
+constexpr int kGemvChunkCols = kGemvChunk * kW4TileCols;
 constexpr int kGemvChunkBytes = kGemvChunk * kW4TileBytes;
 constexpr int kGemvBufferBytes = kGemvWarps * kGemvChunkBytes;
 
@@ -297,15 +298,16 @@ struct ChunkScales {
   }
 };
 
-// acc += one 16 x 128 tile times the activations of eight tokens.  c0, c1:
-// scales of rows g and g + 8; xs: for each group of the chunk, minus the
-// codes' offset times the sum of the activations of tokens 2 t and 2 t + 1;
-// WPG: words (of 32 columns) per group, 8 where a group is two tiles.
-template <typename T, int WPG, int NS>
-__device__ __forceinline__ void gemv_tile(float (&acc)[4], const uint4& w0, const uint4& w1,
-                                          const uint4 (&xv)[4], const ChunkScales<NS>& c0,
+// acc += one 16 x 128 tile times the activations of 8 NT tokens.  x: the
+// lane's activations of the tile, tokens x_next bytes apart from eight to
+// eight; c0, c1: scales of rows g and g + 8; xs: for each group of the chunk,
+// minus the codes' offset times the sum of the activations of tokens 2 t and
+// 2 t + 1; WPG: words (of 32 columns) per group, 8 where a group is two tiles.
+template <typename T, int WPG, int NS, int NT>
+__device__ __forceinline__ void gemv_tile(float (&acc)[NT][4], const uint4& w0, const uint4& w1,
+                                          const uint8_t* x, int x_next, const ChunkScales<NS>& c0,
                                           const ChunkScales<NS>& c1, const float* xs, int tile) {
-  float lower[4], upper[4];         // columns 0 .. 3 and 4 .. 7 of the words
+  float lower[NT][4], upper[NT][4];     // columns 0 .. 3 and 4 .. 7 of the words
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t lo[4], hi[4];
@@ -314,89 +316,105 @@ __device__ __forceinline__ void gemv_tile(float (&acc)[4], const uint4& w0, cons
     const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
     const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
     const int i = (tile * 4 + j) / WPG;
-    if (j % WPG == 0) {
-      float2 o = make_float2(0.0f, 0.0f);         // the second tile of a group goes on
-      if (WPG <= 4 || tile % 2 == 0) o = *reinterpret_cast<const float2*>(xs + 8 * i);
-      const float from[4] = {o.x, o.y, o.x, o.y}, zero[4] = {};
-      Elem<T>::mma(lower, a0, xv[j].x, xv[j].y, from);
-      Elem<T>::mma(upper, a1, xv[j].z, xv[j].w, zero);
-    } else {
-      Elem<T>::mma(lower, a0, xv[j].x, xv[j].y, lower);
-      Elem<T>::mma(upper, a1, xv[j].z, xv[j].w, upper);
-    }
-    if ((j + 1) % WPG == 0 || j == 3) {
-      const float f0 = c0.get(i), f1 = c1.get(i);
-      acc[0] = fmaf(fmaf(upper[0], Elem<T>::kHigh, lower[0]), f0, acc[0]);
-      acc[1] = fmaf(fmaf(upper[1], Elem<T>::kHigh, lower[1]), f0, acc[1]);
-      acc[2] = fmaf(fmaf(upper[2], Elem<T>::kHigh, lower[2]), f1, acc[2]);
-      acc[3] = fmaf(fmaf(upper[3], Elem<T>::kHigh, lower[3]), f1, acc[3]);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint4 xv = *reinterpret_cast<const uint4*>(x + n * x_next + tile * 256 + j * 64);
+      if (j % WPG == 0) {
+        float2 o = make_float2(0.0f, 0.0f);         // the second tile of a group goes on
+        if (WPG <= 4 || tile % 2 == 0) o = *reinterpret_cast<const float2*>(xs + 8 * NT * i + 8 * n);
+        const float from[4] = {o.x, o.y, o.x, o.y}, zero[4] = {};
+        Elem<T>::mma(lower[n], a0, xv.x, xv.y, from);
+        Elem<T>::mma(upper[n], a1, xv.z, xv.w, zero);
+      } else {
+        Elem<T>::mma(lower[n], a0, xv.x, xv.y, lower[n]);
+        Elem<T>::mma(upper[n], a1, xv.z, xv.w, upper[n]);
+      }
+      if ((j + 1) % WPG == 0 || j == 3) {
+        const float f0 = c0.get(i), f1 = c1.get(i);
+        acc[n][0] = fmaf(fmaf(upper[n][0], Elem<T>::kHigh, lower[n][0]), f0, acc[n][0]);
+        acc[n][1] = fmaf(fmaf(upper[n][1], Elem<T>::kHigh, lower[n][1]), f0, acc[n][1]);
+        acc[n][2] = fmaf(fmaf(upper[n][2], Elem<T>::kHigh, lower[n][2]), f1, acc[n][2]);
+        acc[n][3] = fmaf(fmaf(upper[n][3], Elem<T>::kHigh, lower[n][3]), f1, acc[n][3]);
+      }
     }
   }
 }
 
-// Bytes of a token's activations in shared memory: whole tiles (zeros behind
-// K), and half a bank line so that tokens' rows start in different banks.
-__host__ __device__ constexpr int gemv_x_stride(int kbs) { return kbs * kW4TileCols * 2 + 64; }
-
-// The sums of activations are kept for every group of the padded columns.
-__host__ __device__ constexpr int gemv_smem(int M, int kbs, int gs_shift) {
-  return kGemvBufferBytes + M * gemv_x_stride(kbs) +
-         (((kbs * kW4TileCols - 1) >> gs_shift) + 1) * 8 * static_cast<int>(sizeof(float));
+// Chunks of a strip, and those a CTA of a cluster takes at most.
+__host__ __device__ constexpr int gemv_chunks(int kbs) { return (kbs + kGemvChunk - 1) / kGemvChunk; }
+__host__ __device__ constexpr int gemv_share(int kbs, int split) {
+  return (gemv_chunks(kbs) + split - 1) / split;
 }
 
-template <typename T, int WPG>
+// Bytes of a token's activations in shared memory: whole chunks (zeros behind
+// K), and half a bank line so that tokens' rows start in different banks.
+__host__ __device__ constexpr int gemv_x_stride(int chunks) { return chunks * kGemvChunkCols * 2 + 64; }
+
+// Shared memory: the warps' buffers, the activations, their sums per group,
+// and with a cluster its strips' sums.
+__host__ __device__ constexpr long long gemv_smem(int M, int kbs, int gs_shift, int split, int strips) {
+  return kGemvBufferBytes + static_cast<long long>(M) * gemv_x_stride(gemv_share(kbs, split)) +
+         (static_cast<long long>(gemv_share(kbs, split)) * kGemvChunkCols >> gs_shift) * ((M + 7) / 8) * 32 +
+         (split > 1 ? static_cast<long long>(strips) * ((M + 7) / 8) * 512 : 0);
+}
+
+template <typename T, int WPG, int NT>
 __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_constant__ W4Layers L,
                                                                  const W4Args a) {
   constexpr int NS = 4 * kGemvChunk / WPG;        // scales of a row per chunk
   extern __shared__ __align__(128) uint8_t buffers[];
-  const int kbs = a.kbs, x_stride = gemv_x_stride(kbs);
-  uint8_t* xs_mem = buffers + kGemvBufferBytes;                            // [M][x_stride]
-  float* xsum = reinterpret_cast<float*>(xs_mem + a.M * x_stride);        // [groups][8 tokens]
   __shared__ uint64_t full[kGemvWarps];
   __shared__ uint64_t x_full;
-  // [0]: a strip begun by an earlier warp; [1]: one that a later warp ends
-  __shared__ float4 part_of[2][kGemvWarps][32];
+  __shared__ float4 head_of[kGemvWarps][NT][32];  // of a strip begun by an earlier warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rank = blockIdx.x % kGemvCluster;
-  const long long cluster = blockIdx.x / kGemvCluster, clusters = gridDim.x / kGemvCluster;
+  const int kbs = a.kbs, rank = blockIdx.x % a.split;
+  const long long cluster = blockIdx.x / a.split, clusters = gridDim.x / a.split;
   const int strips = L.strip0[L.n];
-  const int per_strip = (kbs + kGemvChunk - 1) / kGemvChunk;
+  // the cluster's strips, and this CTA's chunks of each
   const int first = static_cast<int>(cluster * strips / clusters);
-  const int units = (static_cast<int>((cluster + 1) * strips / clusters) - first) * per_strip;
-  const int share = rank * kGemvWarps + warp;
-  auto begin_of = [&](int w) { return static_cast<int>(static_cast<long long>(w) * units / kGemvShares); };
+  const int count = static_cast<int>((cluster + 1) * strips / clusters) - first;
+  const int per_strip = gemv_chunks(kbs);
+  const int c_lo = rank * per_strip / a.split, chunks = (rank + 1) * per_strip / a.split - c_lo;
+  // tiles of the last of them
+  const int end_tiles = min(kGemvChunk, kbs - (c_lo + chunks - 1) * kGemvChunk);
+  const int units = count * chunks;
+  const int u0 = static_cast<int>(static_cast<long long>(warp) * units / kGemvWarps);
+  const int u1 = static_cast<int>(static_cast<long long>(warp + 1) * units / kGemvWarps);
   auto layer_of = [&](int strip) {
     int l = 0;
     while (l + 1 < L.n && strip >= L.strip0[l + 1]) ++l;
     return l;
   };
-  const int u0 = begin_of(share), u1 = begin_of(share + 1);
+  // shared memory is laid out for the largest share, alike in all CTAs
+  const int room = gemv_share(kbs, a.split), x_stride = gemv_x_stride(room);
   uint8_t* buffer = buffers + warp * kGemvChunkBytes;
-  const int tail_tiles = kbs - (per_strip - 1) * kGemvChunk;              // of a strip's last chunk
+  uint8_t* xs_mem = buffers + kGemvBufferBytes;                           // [M][x_stride]
+  float* xsum = reinterpret_cast<float*>(xs_mem + a.M * x_stride);        // [groups][8 NT tokens]
+  float4* slab = reinterpret_cast<float4*>(xsum + (room * kGemvChunkCols >> a.gs_shift) * 8 * NT);  // [count][NT][32]
 
-  int c = u0 % per_strip, strip = first + u0 / per_strip;   // of the chunk in hand
-  // the next chunk to request, its place in its strip and in memory
+  int c = u0 % chunks, strip = first + u0 / chunks;   // of the chunk in hand
+  // the next chunk to request, its place in the share and in memory
   int ru = u0, rc = c, rs = strip;
   const uint4* rp = nullptr;
   auto stream_at = [&](int strip, int c) {
     const int l = layer_of(strip);
-    return L.wp[l] + (static_cast<size_t>(strip - L.strip0[l]) * kbs + c * kGemvChunk) * (kW4TileBytes / 16);
+    return L.wp[l] + (static_cast<size_t>(strip - L.strip0[l]) * kbs + (c_lo + c) * kGemvChunk) * (kW4TileBytes / 16);
   };
   auto request = [&]() {
     if (ru >= u1) return;
-    const bool end = rc + 1 == per_strip;
-    const int tiles = end ? tail_tiles : kGemvChunk;
+    const bool end = rc + 1 == chunks;
     if (lane == 0) {
-      mbar_arrive_expect_tx(&full[warp], tiles * kW4TileBytes);
-      bulk_load(buffer, rp, tiles * kW4TileBytes, &full[warp]);
+      const uint32_t bytes = (end ? end_tiles : kGemvChunk) * kW4TileBytes;
+      mbar_arrive_expect_tx(&full[warp], bytes);
+      bulk_load(buffer, rp, bytes, &full[warp]);
     }
     ++ru;
     ++rc;
-    rp += tiles * (kW4TileBytes / 16);
+    rp += kGemvChunkBytes / 16;
     if (end) {
       rc = 0;
       ++rs;
-      if (L.n > 1 && ru < u1) rp = stream_at(rs, 0);        // perhaps another layer's
+      if (ru < u1) rp = stream_at(rs, 0);
     }
   };
   if (u0 < u1) rp = stream_at(strip, c);
@@ -409,16 +427,16 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   request();
 
   // where the scales of rows g and g + 8 lie, from the next chunk on
-  const bool even = a.K % (kGemvChunk * kW4TileCols) == 0;
+  const bool even = a.K % kGemvChunkCols == 0;
   const __half *p0 = nullptr, *p1 = nullptr;
   int left0 = 0, left1 = 0;                       // of the row; none behind the last row
   auto rows_of = [&](int strip, int c) {
     const int l = layer_of(strip);
-    const int row = (strip - L.strip0[l]) * 16 + g;
-    p0 = L.ws[l] + static_cast<size_t>(row) * a.G + c * NS;
+    const int row = (strip - L.strip0[l]) * 16 + g, at = (c_lo + c) * NS;
+    p0 = L.ws[l] + static_cast<size_t>(row) * a.G + at;
     p1 = p0 + static_cast<size_t>(8) * a.G;
-    left0 = row < L.N[l] ? a.G - c * NS : 0;
-    left1 = row + 8 < L.N[l] ? a.G - c * NS : 0;
+    left0 = row < L.N[l] ? a.G - at : 0;
+    left1 = row + 8 < L.N[l] ? a.G - at : 0;
   };
   ChunkScales<NS> c0, c1, n0, n1;
   if (u0 < u1) {
@@ -427,7 +445,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     c1.load(p1, left1, even);
   }
   // activations to shared memory; columns behind K are zeros
-  const int row_bytes = a.K * 2, pad16 = (kbs * kW4TileCols * 2 - row_bytes) / 16;
+  const int padded = chunks * kGemvChunkCols;
+  const int row_bytes = min(padded, a.K - c_lo * kGemvChunkCols) * 2, pad16 = (padded * 2 - row_bytes) / 16;
   for (int i = threadIdx.x; i < a.M * pad16; i += kGemvThreads)
     *reinterpret_cast<uint4*>(xs_mem + i / pad16 * x_stride + row_bytes + i % pad16 * 16) = make_uint4(0, 0, 0, 0);
   grid_launch_dependents();
@@ -435,7 +454,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   if (threadIdx.x == 0) {
     mbar_arrive_expect_tx(&x_full, a.M * row_bytes);
     for (int m = 0; m < a.M; ++m)
-      bulk_load(xs_mem + m * x_stride, static_cast<const T*>(a.x) + m * a.ldx, row_bytes, &x_full);
+      bulk_load(xs_mem + m * x_stride, static_cast<const T*>(a.x) + m * a.ldx + c_lo * kGemvChunkCols,
+                row_bytes, &x_full);
   }
   __syncthreads();                  // x_full is initialised; the padding is written
   bool ok = __syncthreads_and(mbar_wait(&x_full, 0, a.wait_limit_ns));
@@ -443,41 +463,49 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
 
   // the sums of the activations of each token and group, gs / 8 lanes to a
   // group; behind K they are zero like the scales there
-  const int padded = kbs * kW4TileCols, vecs = (padded / 8 + 31) / 32 * 32;
+  const int vecs = padded / 8;      // a multiple of 64
   for (int i = threadIdx.x; i < a.M * vecs; i += kGemvThreads) {
     const int m = i / vecs, k = (i - m * vecs) * 8;
-    float sum = 0.0f;
-    if (k < padded) {
-      const uint4 v = *reinterpret_cast<const uint4*>(xs_mem + m * x_stride + k * 2);
-      const float2 q0 = Elem<T>::unpack(v.x), q1 = Elem<T>::unpack(v.y);
-      const float2 q2 = Elem<T>::unpack(v.z), q3 = Elem<T>::unpack(v.w);
-      sum = ((q0.x + q0.y) + (q1.x + q1.y)) + ((q2.x + q2.y) + (q3.x + q3.y));
-    }
+    const uint4 v = *reinterpret_cast<const uint4*>(xs_mem + m * x_stride + k * 2);
+    const float2 q0 = Elem<T>::unpack(v.x), q1 = Elem<T>::unpack(v.y);
+    const float2 q2 = Elem<T>::unpack(v.z), q3 = Elem<T>::unpack(v.w);
+    float sum = ((q0.x + q0.y) + (q1.x + q1.y)) + ((q2.x + q2.y) + (q3.x + q3.y));
 #pragma unroll
     for (int o = 2 * WPG; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (k < padded && lane % (4 * WPG) == 0) xsum[(k >> a.gs_shift) * 8 + m] = -Elem<T>::kOffset * sum;
+    if (lane % (4 * WPG) == 0) xsum[(k >> a.gs_shift) * 8 * NT + m] = -Elem<T>::kOffset * sum;
   }
   __syncthreads();
 
   // a column of the product without a token is computed and dropped
   const uint8_t* x = xs_mem + min(g, a.M - 1) * x_stride + t * 16;
-  auto store = [&](int strip, const float (&v)[4]) {
+  const int x_next = NT > 1 ? (min(g + 8, a.M - 1) - g) * x_stride : 0;
+  auto store = [&](int strip, int n, const float4& f) {
     const int l = layer_of(strip);
     const int row = (strip - L.strip0[l]) * 16 + g;
     T* y = static_cast<T*>(L.y[l]) + row;
+    const float v[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int m = 2 * t + (i & 1);
+      const int m = n * 8 + 2 * t + (i & 1);
       if (m < a.M && row + 8 * (i >> 1) < L.N[l])
         y[m * L.ldy[l] + 8 * (i >> 1)] = Elem<T>::from_float(v[i] * Elem<T>::kUnit);
     }
   };
-  float acc[4] = {};
+  // a CTA's sums of a strip: results without a cluster
+  auto finish = [&](int strip, const float (&v)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float4 f = make_float4(v[n][0], v[n][1], v[n][2], v[n][3]);
+      if (a.split == 1) store(strip, n, f);
+      else slab[((strip - first) * NT + n) * 32 + lane] = f;
+    }
+  };
+  float acc[NT][4] = {};
   bool whole = c == 0;              // the strip's first chunk is this warp's
   uint32_t parity = 0;
 #pragma unroll 1
   for (int u = u0; ok && u < u1; ++u, parity ^= 1) {
-    const bool end = c + 1 == per_strip;
+    const bool end = c + 1 == chunks;
     if (u + 1 < u1) {               // the next chunk's scales
       if (end) {
         rows_of(strip + 1, 0);
@@ -506,28 +534,31 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     }
     __syncwarp();                   // every lane holds the chunk
     request();                      // the next one comes while this one is multiplied
-    const uint4* xp = reinterpret_cast<const uint4*>(x + c * (kGemvChunk * kW4TileCols * 2));
-    const float* xs = xsum + c * NS * 8 + 2 * t;
-    auto multiply = [&](int i) {
-      const uint4 xv[4] = {xp[i * 16], xp[i * 16 + 4], xp[i * 16 + 8], xp[i * 16 + 12]};
-      gemv_tile<T, WPG, NS>(acc, w[i][0], w[i][1], xv, c0, c1, xs, i);
-    };
-    if (!end || tail_tiles == kGemvChunk) {
+    const uint8_t* xp = x + c * (kGemvChunkCols * 2);
+    const float* xs = xsum + c * NS * 8 * NT + 2 * t;
+    if (!end || end_tiles == kGemvChunk) {
 #pragma unroll
-      for (int i = 0; i < kGemvChunk; ++i) multiply(i);
+      for (int i = 0; i < kGemvChunk; ++i)
+        gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, x_next, c0, c1, xs, i);
     } else {
 #pragma unroll
       for (int i = 0; i < kGemvChunk; ++i)
-        if (i < tail_tiles) multiply(i);
+        if (i < end_tiles) gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, x_next, c0, c1, xs, i);
     }
     c0 = n0;
     c1 = n1;
     ++c;
     if (end) {
-      if (whole) store(strip, acc);
-      else part_of[0][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (whole) {
+        finish(strip, acc);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          head_of[warp][n][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+      }
       whole = true;
-      acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
       c = 0;
       ++strip;
     }
@@ -537,35 +568,55 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     if (ru > u0) mbar_wait(&full[warp], (ru - u0 - 1) & 1, a.wait_limit_ns);
   }
   const bool open = u0 < u1 && c > 0;           // the last strip goes on behind this warp
-  if (open) part_of[whole ? 1 : 0][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  cluster_sync_all();
+  if (open && !whole) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      head_of[warp][n][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+  }
+  __syncthreads();
   if (open && whole) {
-    const int end = (strip - first + 1) * per_strip;
-    constexpr int kBatch = 8;       // loads from the other warps in flight
-    for (int w0 = share + 1; w0 < kGemvShares && begin_of(w0) < end; w0 += kBatch) {
-      float4 v[kBatch];
+    const int end = (strip - first + 1) * chunks;
+    for (int w2 = warp + 1; w2 < kGemvWarps; ++w2) {
+      const int b0 = static_cast<int>(static_cast<long long>(w2) * units / kGemvWarps);
+      const int b1 = static_cast<int>(static_cast<long long>(w2 + 1) * units / kGemvWarps);
+      if (b0 >= end) break;
+      if (b0 == b1) continue;                   // a warp without chunks
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int w2 = w0 + i;
-        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        // a warp without chunks has nothing to add
-        if (w2 < kGemvShares && begin_of(w2) < end && begin_of(w2) < begin_of(w2 + 1))
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(v[i].x), "=f"(v[i].y), "=f"(v[i].z), "=f"(v[i].w)
-                       : "r"(map_to_rank(smem_u32(&part_of[0][w2 % kGemvWarps][lane]), w2 / kGemvWarps))
-                       : "memory");
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        acc[0] += v[i].x;
-        acc[1] += v[i].y;
-        acc[2] += v[i].z;
-        acc[3] += v[i].w;
+      for (int n = 0; n < NT; ++n) {
+        const float4 v = head_of[w2][n][lane];
+        acc[n][0] += v.x;
+        acc[n][1] += v.y;
+        acc[n][2] += v.z;
+        acc[n][3] += v.w;
       }
     }
-    store(strip, acc);
+    finish(strip, acc);
   }
-  cluster_sync_all();               // no CTA leaves while another reads its part
+  if (a.split == 1) return;
+  cluster_sync_all();
+  // the ranks' sums of every strip, a share of them each
+  for (int i = rank * kGemvWarps + warp; i < count * NT; i += a.split * kGemvWarps) {
+    const uint32_t at = smem_u32(slab + i * 32 + lane);
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 v[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (r < a.split)
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                     : "r"(map_to_rank(at, r)) : "memory");
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      sum.x += v[r].x;
+      sum.y += v[r].y;
+      sum.z += v[r].z;
+      sum.w += v[r].w;
+    }
+    store(first + i / NT, i % NT, sum);
+  }
+  cluster_sync_all();               // no CTA leaves while another reads its sums
 }
 
 }  // namespace flexq

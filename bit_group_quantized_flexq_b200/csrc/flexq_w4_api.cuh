@@ -30,8 +30,10 @@ size_t w4_packed_bytes(int N, int K) {
 }
 
 // ----------------------------------------------------------- linear layers --
-constexpr int kGemvTokens = 8;    // batches of the streaming kernel
-constexpr int kGemvSmem = 208 * 1024;   // its buffers, activations and their sums
+constexpr int kGemvTokens = 16;          // batches of the streaming kernel
+// and the shared memory it may ask for: an SM's 227 KB less its static arrays
+// (the warps' partial sums and the barriers)
+constexpr int gemv_smem_limit(int M) { return 227 * 1024 - 256 - (M + 7) / 8 * flexq::kGemvWarps * 512; }
 
 // Lets a kernel use more than 48 KB of shared memory, once per device.
 template <typename Kernel>
@@ -46,43 +48,96 @@ cudaError_t allow_smem(Kernel kern, int bytes, bool (&done)[kMaxDevices]) {
   return e;
 }
 
-template <typename T, int WPG>
-cudaError_t launch_gemv(const flexq::W4Layers& L, const flexq::W4Args& a, int sms, cudaStream_t stream) {
-  static bool ready[kMaxDevices];
-  const cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG>, kGemvSmem, ready);
-  if (e != cudaSuccess) return e;
-  // one cluster per pair of SMs, and none without a strip
-  const int clusters = std::max(1, std::min(L.strip0[L.n], sms / 2));
+template <typename T, int WPG, int NT>
+cudaLaunchConfig_t gemv_config(unsigned ctas, int split, size_t smem, cudaLaunchAttribute (&attr)[2],
+                               cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * flexq::kGemvCluster));
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(flexq::kGemvThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(flexq::gemv_smem(a.M, a.kbs, a.gs_shift));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = flexq::kGemvCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
   // the first weights are requested while the previous kernel finishes
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG>, L, a);
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cfg;
 }
 
-template <typename T>
-cudaError_t launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, int sms,
-                           cudaStream_t stream) {
-  return gs == 32    ? launch_gemv<T, 1>(L, a, sms, stream)
-         : gs == 64  ? launch_gemv<T, 2>(L, a, sms, stream)
-         : gs == 128 ? launch_gemv<T, 4>(L, a, sms, stream)
-                     : launch_gemv<T, 8>(L, a, sms, stream);
+// Clusters of 1, 2, 4 and 8 CTAs that run at once, one CTA per SM (asked once
+// per device; 0 where the driver has no place for any).
+template <typename T, int WPG, int NT>
+cudaError_t gemv_clusters(int sms, const int (*&clusters)[4]) {
+  static int known[kMaxDevices][4];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_dev_mutex);
+  if (known[dev][0] == 0) {
+    int n[4] = {sms, 0, 0, 0};
+    for (int i = 1; i < 4; ++i) {
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(1u << i, 1 << i, gemv_smem_limit(8 * NT), attr, nullptr);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&n[i], flexq::w4_gemv_kernel<T, WPG, NT>, &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    memcpy(known[dev], n, sizeof(n));
+  }
+  clusters = &known[dev];
+  return cudaSuccess;
 }
 
-// Whether a launch's activations fit the streaming kernel's shared memory.
-bool gemv_fits(const flexq::W4Args& a) {
-  return a.K <= 65536 && flexq::gemv_smem(a.M, a.kbs, a.gs_shift) <= kGemvSmem;
+// CTAs of a cluster (1, 2, 4 or 8) and clusters of a launch: the fewest chunks
+// for the CTA that has most of them, among those whose activations fit shared
+// memory; false where none do.
+bool gemv_plan(const flexq::W4Args& a, int strips, const int (&clusters)[4], int* split, int* used) {
+  long long best = -1;
+  for (int i = 0; i < 4; ++i) {
+    const int s = 1 << i, n = std::min(strips, clusters[i]);
+    if (n == 0 || s > flexq::gemv_chunks(a.kbs)) continue;
+    const int most = (strips + n - 1) / n;
+    if (flexq::gemv_smem(a.M, a.kbs, a.gs_shift, s, most) > gemv_smem_limit(a.M)) continue;
+    const long long units = static_cast<long long>(most) * flexq::gemv_share(a.kbs, s);
+    if (best >= 0 && units >= best) continue;
+    best = units;
+    *split = s;
+    *used = n;
+  }
+  return best > 0 && best <= INT32_MAX;
+}
+
+// FLEXQ_OK and *done where the streaming kernel took the batch.
+template <typename T, int WPG, int NT>
+int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, int sms, cudaStream_t stream, bool* done) {
+  static bool ready[kMaxDevices];
+  cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT>, gemv_smem_limit(8 * NT), ready);
+  const int (*clusters)[4] = nullptr;
+  if (e == cudaSuccess) e = gemv_clusters<T, WPG, NT>(sms, clusters);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit linear set-up");
+  int used = 0;
+  *done = a.K <= (1 << 20) && gemv_plan(a, L.strip0[L.n], *clusters, &a.split, &used);
+  if (!*done) return FLEXQ_OK;
+  const long long smem = flexq::gemv_smem(a.M, a.kbs, a.gs_shift, a.split, (L.strip0[L.n] + used - 1) / used);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(static_cast<unsigned>(used * a.split), a.split,
+                                                         static_cast<size_t>(smem), attr, stream);
+  e = cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG, NT>, L, a);
+  return e == cudaSuccess ? FLEXQ_OK : cuda_fail(e, "4-bit linear launch");
+}
+
+template <typename T, int NT>
+int launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, int sms, cudaStream_t stream,
+                   bool* done) {
+  return gs == 32    ? launch_gemv<T, 1, NT>(L, a, sms, stream, done)
+         : gs == 64  ? launch_gemv<T, 2, NT>(L, a, sms, stream, done)
+         : gs == 128 ? launch_gemv<T, 4, NT>(L, a, sms, stream, done)
+                     : launch_gemv<T, 8, NT>(L, a, sms, stream, done);
 }
 
 // ---- batches beyond those: the tcgen05 kernel ----
@@ -169,9 +224,11 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
 
 template <typename E>
 int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, int sms, cudaStream_t s) {
-  if (a.M <= kGemvTokens && gemv_fits(a)) {
-    const cudaError_t e = launch_gemv_gs<E>(gs, L, a, sms, s);
-    return e == cudaSuccess ? FLEXQ_OK : cuda_fail(e, "4-bit linear launch");
+  if (a.M <= kGemvTokens) {
+    bool done = false;
+    const int rc = a.M <= 8 ? launch_gemv_gs<E, 1>(gs, L, a, sms, s, &done)
+                            : launch_gemv_gs<E, 2>(gs, L, a, sms, s, &done);
+    if (rc || done) return rc;
   }
   flexq::W4MmaArgs m;
   memset(&m, 0, sizeof(m));

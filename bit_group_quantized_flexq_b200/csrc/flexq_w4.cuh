@@ -226,7 +226,7 @@ struct W4Args {
   const void* x;
   long long ldx;
   int M, K, G, kbs, gs_shift;     // kbs: tiles of 128 columns; gs = 1 << gs_shift
-  int split;                      // streaming kernel: CTAs of a cluster
+  int split, rounds;              // streaming kernel: CTAs of a cluster, parts of its strips
   unsigned int* status;           // device status word
   unsigned long long wait_limit_ns;
 };
@@ -243,7 +243,9 @@ struct W4Args {
 // and BF16; the tensor core adds a group's products in FP32, and the group's
 // sum times the scale is added in FP32.  What a warp has of a strip that it
 // shares with others is added, in the order of the columns, by the warp that
-// holds the strip's first chunk, and so are the CTAs' sums of a strip.
+// holds the strip's first chunk, and so are the CTAs' sums of a strip.  Where
+// shared memory does not hold those of all its strips, a cluster takes them in
+// rounds.
 //
 // Taking a code apart has to cost little: at HBM's rate an SM has about 44
 // cycles per tile.  So the tensor core multiplies codes with an offset, u = q
@@ -299,13 +301,14 @@ struct ChunkScales {
 };
 
 // acc += one 16 x 128 tile times the activations of 8 NT tokens.  x: the
-// lane's activations of the tile, tokens x_next bytes apart from eight to
-// eight; c0, c1: scales of rows g and g + 8; xs: for each group of the chunk,
+// lane's activations of the chunk, those of the n-th eight tokens xo[n] bytes
+// on; c0, c1: scales of rows g and g + 8; xs: for each group of the chunk,
 // minus the codes' offset times the sum of the activations of tokens 2 t and
 // 2 t + 1; WPG: words (of 32 columns) per group, 8 where a group is two tiles.
 template <typename T, int WPG, int NS, int NT>
 __device__ __forceinline__ void gemv_tile(float (&acc)[NT][4], const uint4& w0, const uint4& w1,
-                                          const uint8_t* x, int x_next, const ChunkScales<NS>& c0,
+                                          const uint8_t* x, const int (&xo)[NT],
+                                          const ChunkScales<NS>& c0,
                                           const ChunkScales<NS>& c1, const float* xs, int tile) {
   float lower[NT][4], upper[NT][4];     // columns 0 .. 3 and 4 .. 7 of the words
 #pragma unroll
@@ -318,7 +321,7 @@ __device__ __forceinline__ void gemv_tile(float (&acc)[NT][4], const uint4& w0, 
     const int i = (tile * 4 + j) / WPG;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const uint4 xv = *reinterpret_cast<const uint4*>(x + n * x_next + tile * 256 + j * 64);
+      const uint4 xv = *reinterpret_cast<const uint4*>(x + xo[n] + tile * 256 + j * 64);
       if (j % WPG == 0) {
         float2 o = make_float2(0.0f, 0.0f);         // the second tile of a group goes on
         if (WPG <= 4 || tile % 2 == 0) o = *reinterpret_cast<const float2*>(xs + 8 * NT * i + 8 * n);
@@ -350,15 +353,20 @@ __host__ __device__ constexpr int gemv_share(int kbs, int split) {
 // K), and half a bank line so that tokens' rows start in different banks.
 __host__ __device__ constexpr int gemv_x_stride(int chunks) { return chunks * kGemvChunkCols * 2 + 64; }
 
+// Eights of tokens that the kernel multiplies at once.
+__host__ __device__ constexpr int gemv_eights(int M) { return M <= 8 ? 1 : 2; }
+
 // Shared memory: the warps' buffers, the activations, their sums per group,
-// and with a cluster its strips' sums.
+// and with a cluster the sums of the strips of a round.
 __host__ __device__ constexpr long long gemv_smem(int M, int kbs, int gs_shift, int split, int strips) {
   return kGemvBufferBytes + static_cast<long long>(M) * gemv_x_stride(gemv_share(kbs, split)) +
-         (static_cast<long long>(gemv_share(kbs, split)) * kGemvChunkCols >> gs_shift) * ((M + 7) / 8) * 32 +
-         (split > 1 ? static_cast<long long>(strips) * ((M + 7) / 8) * 512 : 0);
+         (static_cast<long long>(gemv_share(kbs, split)) * kGemvChunkCols >> gs_shift) * gemv_eights(M) * 32 +
+         (split > 1 ? static_cast<long long>(strips) * gemv_eights(M) * 512 : 0);
 }
 
-template <typename T, int WPG, int NT>
+// MANY: several rounds (a kernel of its own: the loop costs one round's launch
+// of 4096 x 4096 at one token 0.4 of 5.3 us).
+template <typename T, int WPG, int NT, bool MANY>
 __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_constant__ W4Layers L,
                                                                  const W4Args a) {
   constexpr int NS = 4 * kGemvChunk / WPG;        // scales of a row per chunk
@@ -371,15 +379,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   const long long cluster = blockIdx.x / a.split, clusters = gridDim.x / a.split;
   const int strips = L.strip0[L.n];
   // the cluster's strips, and this CTA's chunks of each
-  const int first = static_cast<int>(cluster * strips / clusters);
-  const int count = static_cast<int>((cluster + 1) * strips / clusters) - first;
+  const int strip_lo = static_cast<int>(cluster * strips / clusters);
+  const int strip_n = static_cast<int>((cluster + 1) * strips / clusters) - strip_lo;
   const int per_strip = gemv_chunks(kbs);
   const int c_lo = rank * per_strip / a.split, chunks = (rank + 1) * per_strip / a.split - c_lo;
   // tiles of the last of them
   const int end_tiles = min(kGemvChunk, kbs - (c_lo + chunks - 1) * kGemvChunk);
-  const int units = count * chunks;
-  const int u0 = static_cast<int>(static_cast<long long>(warp) * units / kGemvWarps);
-  const int u1 = static_cast<int>(static_cast<long long>(warp + 1) * units / kGemvWarps);
   auto layer_of = [&](int strip) {
     int l = 0;
     while (l + 1 < L.n && strip >= L.strip0[l + 1]) ++l;
@@ -392,9 +397,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   float* xsum = reinterpret_cast<float*>(xs_mem + a.M * x_stride);        // [groups][8 NT tokens]
   float4* slab = reinterpret_cast<float4*>(xsum + (room * kGemvChunkCols >> a.gs_shift) * 8 * NT);  // [count][NT][32]
 
-  int c = u0 % chunks, strip = first + u0 / chunks;   // of the chunk in hand
+  int first, count, units;          // the round's strips and this CTA's chunks of them
+  int u0, u1;                       // this warp's chunks
+  int c, strip;                     // of the chunk in hand
   // the next chunk to request, its place in the share and in memory
-  int ru = u0, rc = c, rs = strip;
+  int ru, rc, rs, asked = 0;
   const uint4* rp = nullptr;
   auto stream_at = [&](int strip, int c) {
     const int l = layer_of(strip);
@@ -408,6 +415,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
       mbar_arrive_expect_tx(&full[warp], bytes);
       bulk_load(buffer, rp, bytes, &full[warp]);
     }
+    ++asked;
     ++ru;
     ++rc;
     rp += kGemvChunkBytes / 16;
@@ -417,14 +425,29 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
       if (ru < u1) rp = stream_at(rs, 0);
     }
   };
-  if (u0 < u1) rp = stream_at(strip, c);
+  auto begin = [&](int round) {
+    first = strip_lo;
+    count = strip_n;
+    if (MANY) {
+      first += static_cast<int>(static_cast<long long>(round) * strip_n / a.rounds);
+      count = strip_lo + static_cast<int>(static_cast<long long>(round + 1) * strip_n / a.rounds) - first;
+    }
+    units = count * chunks;
+    u0 = static_cast<int>(static_cast<long long>(warp) * units / kGemvWarps);
+    u1 = static_cast<int>(static_cast<long long>(warp + 1) * units / kGemvWarps);
+    ru = u0;
+    rc = c = u0 % chunks;
+    rs = strip = first + u0 / chunks;
+    if (u0 < u1) rp = stream_at(strip, c);
+    request();
+  };
   if (lane == 0) {
     mbar_init(&full[warp], 1);
     if (warp == 0) mbar_init(&x_full, 1);
     fence_barrier_init();
   }
   __syncwarp();
-  request();
+  begin(0);
 
   // where the scales of rows g and g + 8 lie, from the next chunk on
   const bool even = a.K % kGemvChunkCols == 0;
@@ -439,11 +462,13 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     left1 = row + 8 < L.N[l] ? a.G - at : 0;
   };
   ChunkScales<NS> c0, c1, n0, n1;
-  if (u0 < u1) {
+  auto first_scales = [&]() {
+    if (u0 >= u1) return;
     rows_of(strip, c);
     c0.load(p0, left0, even);
     c1.load(p1, left1, even);
-  }
+  };
+  first_scales();
   // activations to shared memory; columns behind K are zeros
   const int padded = chunks * kGemvChunkCols;
   const int row_bytes = min(padded, a.K - c_lo * kGemvChunkCols) * 2, pad16 = (padded * 2 - row_bytes) / 16;
@@ -478,7 +503,9 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
 
   // a column of the product without a token is computed and dropped
   const uint8_t* x = xs_mem + min(g, a.M - 1) * x_stride + t * 16;
-  const int x_next = NT > 1 ? (min(g + 8, a.M - 1) - g) * x_stride : 0;
+  int xo[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xo[n] = g + 8 * n < a.M ? 8 * n * x_stride : 0;
   auto store = [&](int strip, int n, const float4& f) {
     const int l = layer_of(strip);
     const int row = (strip - L.strip0[l]) * 16 + g;
@@ -500,9 +527,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
       else slab[((strip - first) * NT + n) * 32 + lane] = f;
     }
   };
+  uint32_t parity = 0;
+#pragma unroll 1
+  for (int round = 0;;) {
   float acc[NT][4] = {};
   bool whole = c == 0;              // the strip's first chunk is this warp's
-  uint32_t parity = 0;
 #pragma unroll 1
   for (int u = u0; ok && u < u1; ++u, parity ^= 1) {
     const bool end = c + 1 == chunks;
@@ -539,11 +568,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     if (!end || end_tiles == kGemvChunk) {
 #pragma unroll
       for (int i = 0; i < kGemvChunk; ++i)
-        gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, x_next, c0, c1, xs, i);
+        gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, xo, c0, c1, xs, i);
     } else {
 #pragma unroll
       for (int i = 0; i < kGemvChunk; ++i)
-        if (i < end_tiles) gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, x_next, c0, c1, xs, i);
+        if (i < end_tiles) gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, xo, c0, c1, xs, i);
     }
     c0 = n0;
     c1 = n1;
@@ -565,7 +594,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   }
   if (!ok) {                        // let the copies in flight land
     mbar_wait(&x_full, 0, a.wait_limit_ns);
-    if (ru > u0) mbar_wait(&full[warp], (ru - u0 - 1) & 1, a.wait_limit_ns);
+    if (asked > 0) mbar_wait(&full[warp], (asked - 1) & 1, a.wait_limit_ns);
   }
   const bool open = u0 < u1 && c > 0;           // the last strip goes on behind this warp
   if (open && !whole) {
@@ -592,10 +621,15 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     }
     finish(strip, acc);
   }
-  if (a.split == 1) return;
+  if (a.split == 1) return;         // in one round
+  const int round_first = first, round_count = count;
+  if (MANY && ++round < a.rounds) { // its first chunk comes while the sums are added
+    begin(round);
+    first_scales();
+  }
   cluster_sync_all();
   // the ranks' sums of every strip, a share of them each
-  for (int i = rank * kGemvWarps + warp; i < count * NT; i += a.split * kGemvWarps) {
+  for (int i = rank * kGemvWarps + warp; i < round_count * NT; i += a.split * kGemvWarps) {
     const uint32_t at = smem_u32(slab + i * 32 + lane);
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float4 v[8];
@@ -614,9 +648,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
       sum.z += v[r].z;
       sum.w += v[r].w;
     }
-    store(first + i / NT, i % NT, sum);
+    store(round_first + i / NT, i % NT, sum);
   }
-  cluster_sync_all();               // no CTA leaves while another reads its sums
+  // no CTA leaves, or writes its sums again, while another reads them
+  cluster_sync_all();
+  if (!MANY || round == a.rounds) return;
+  }
 }
 
 }  // namespace flexq

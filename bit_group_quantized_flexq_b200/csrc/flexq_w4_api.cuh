@@ -33,7 +33,9 @@ size_t w4_packed_bytes(int N, int K) {
 constexpr int kGemvTokens = 16;          // batches of the streaming kernel
 // and the shared memory it may ask for: an SM's 227 KB less its static arrays
 // (the warps' partial sums and the barriers)
-constexpr int gemv_smem_limit(int M) { return 227 * 1024 - 256 - (M + 7) / 8 * flexq::kGemvWarps * 512; }
+constexpr int gemv_smem_limit(int M) {
+  return 227 * 1024 - 256 - flexq::gemv_eights(M) * flexq::kGemvWarps * 512;
+}
 
 // Lets a kernel use more than 48 KB of shared memory, once per device.
 template <typename Kernel>
@@ -84,7 +86,7 @@ cudaError_t gemv_clusters(int sms, const int (*&clusters)[4]) {
       cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(1u << i, 1 << i, gemv_smem_limit(8 * NT), attr, nullptr);
       cfg.attrs = attr + 1;
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&n[i], flexq::w4_gemv_kernel<T, WPG, NT>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n[i], flexq::w4_gemv_kernel<T, WPG, NT, false>, &cfg);
       if (e != cudaSuccess) return e;
     }
     memcpy(known[dev], n, sizeof(n));
@@ -93,51 +95,70 @@ cudaError_t gemv_clusters(int sms, const int (*&clusters)[4]) {
   return cudaSuccess;
 }
 
-// CTAs of a cluster (1, 2, 4 or 8) and clusters of a launch: the fewest chunks
-// for the CTA that has most of them, among those whose activations fit shared
-// memory; false where none do.
-bool gemv_plan(const flexq::W4Args& a, int strips, const int (&clusters)[4], int* split, int* used) {
+// Whether the streaming kernel takes a batch: by its size, and by whether the
+// share of its activations of some cluster's CTA fits shared memory.
+bool gemv_takes(int M, int kbs, int gs_shift) {
+  if (M > kGemvTokens || kbs > (1 << 13)) return false;
+  for (int s = 1; s <= 8 && s <= flexq::gemv_chunks(kbs); s *= 2)
+    if (flexq::gemv_smem(M, kbs, gs_shift, s, 1) <= gemv_smem_limit(M)) return true;
+  return false;
+}
+
+// CTAs of a cluster (1, 2, 4 or 8), clusters of a launch and rounds: the
+// fewest chunks for the CTA that has most of them, a round more counted as two
+// chunks per warp.
+struct GemvPlan {
+  int split, clusters, rounds;
+  long long smem;
+};
+
+bool gemv_plan(const flexq::W4Args& a, int strips, const int (&clusters)[4], GemvPlan* plan) {
   long long best = -1;
   for (int i = 0; i < 4; ++i) {
     const int s = 1 << i, n = std::min(strips, clusters[i]);
     if (n == 0 || s > flexq::gemv_chunks(a.kbs)) continue;
-    const int most = (strips + n - 1) / n;
-    if (flexq::gemv_smem(a.M, a.kbs, a.gs_shift, s, most) > gemv_smem_limit(a.M)) continue;
-    const long long units = static_cast<long long>(most) * flexq::gemv_share(a.kbs, s);
-    if (best >= 0 && units >= best) continue;
+    const long long room = gemv_smem_limit(a.M);
+    const int most = (strips + n - 1) / n, share = flexq::gemv_share(a.kbs, s);
+    int rounds = 1;
+    auto of_a_round = [&] { return (most + rounds - 1) / rounds; };
+    while (rounds < most && flexq::gemv_smem(a.M, a.kbs, a.gs_shift, s, of_a_round()) > room) ++rounds;
+    const long long smem = flexq::gemv_smem(a.M, a.kbs, a.gs_shift, s, of_a_round());
+    if (smem > room) continue;
+    const long long units = static_cast<long long>(most) * share + (rounds - 1) * 2 * flexq::kGemvWarps;
+    if (units > INT32_MAX || (best >= 0 && units >= best)) continue;
     best = units;
-    *split = s;
-    *used = n;
+    *plan = {s, n, rounds, smem};
   }
-  return best > 0 && best <= INT32_MAX;
+  return best > 0;
 }
 
-// FLEXQ_OK and *done where the streaming kernel took the batch.
 template <typename T, int WPG, int NT>
-int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, int sms, cudaStream_t stream, bool* done) {
-  static bool ready[kMaxDevices];
-  cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT>, gemv_smem_limit(8 * NT), ready);
+int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, int sms, cudaStream_t stream) {
+  static bool ready[2][kMaxDevices];
+  cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT, false>, gemv_smem_limit(8 * NT), ready[0]);
+  if (e == cudaSuccess) e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT, true>, gemv_smem_limit(8 * NT), ready[1]);
   const int (*clusters)[4] = nullptr;
   if (e == cudaSuccess) e = gemv_clusters<T, WPG, NT>(sms, clusters);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit linear set-up");
-  int used = 0;
-  *done = a.K <= (1 << 20) && gemv_plan(a, L.strip0[L.n], *clusters, &a.split, &used);
-  if (!*done) return FLEXQ_OK;
-  const long long smem = flexq::gemv_smem(a.M, a.kbs, a.gs_shift, a.split, (L.strip0[L.n] + used - 1) / used);
+  GemvPlan p;
+  if (!gemv_plan(a, L.strip0[L.n], *clusters, &p))
+    return fail(FLEXQ_ERR_UNSUPPORTED, "no launch for %d tokens, %d strips, K=%d", a.M, L.strip0[L.n], a.K);
+  a.split = p.split;
+  a.rounds = p.rounds;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(static_cast<unsigned>(used * a.split), a.split,
-                                                         static_cast<size_t>(smem), attr, stream);
-  e = cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG, NT>, L, a);
+  const cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(static_cast<unsigned>(p.clusters * p.split), p.split,
+                                                         static_cast<size_t>(p.smem), attr, stream);
+  e = p.rounds == 1 ? cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG, NT, false>, L, a)
+                    : cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG, NT, true>, L, a);
   return e == cudaSuccess ? FLEXQ_OK : cuda_fail(e, "4-bit linear launch");
 }
 
 template <typename T, int NT>
-int launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, int sms, cudaStream_t stream,
-                   bool* done) {
-  return gs == 32    ? launch_gemv<T, 1, NT>(L, a, sms, stream, done)
-         : gs == 64  ? launch_gemv<T, 2, NT>(L, a, sms, stream, done)
-         : gs == 128 ? launch_gemv<T, 4, NT>(L, a, sms, stream, done)
-                     : launch_gemv<T, 8, NT>(L, a, sms, stream, done);
+int launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, int sms, cudaStream_t stream) {
+  return gs == 32    ? launch_gemv<T, 1, NT>(L, a, sms, stream)
+         : gs == 64  ? launch_gemv<T, 2, NT>(L, a, sms, stream)
+         : gs == 128 ? launch_gemv<T, 4, NT>(L, a, sms, stream)
+                     : launch_gemv<T, 8, NT>(L, a, sms, stream);
 }
 
 // ---- batches beyond those: the tcgen05 kernel ----
@@ -224,11 +245,9 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
 
 template <typename E>
 int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, int sms, cudaStream_t s) {
-  if (a.M <= kGemvTokens) {
-    bool done = false;
-    const int rc = a.M <= 8 ? launch_gemv_gs<E, 1>(gs, L, a, sms, s, &done)
-                            : launch_gemv_gs<E, 2>(gs, L, a, sms, s, &done);
-    if (rc || done) return rc;
+  if (gemv_takes(a.M, a.kbs, a.gs_shift)) {
+    return flexq::gemv_eights(a.M) == 1 ? launch_gemv_gs<E, 1>(gs, L, a, sms, s)
+                                        : launch_gemv_gs<E, 2>(gs, L, a, sms, s);
   }
   flexq::W4MmaArgs m;
   memset(&m, 0, sizeof(m));
@@ -406,6 +425,11 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "4-bit quantizer launch");
   return ok();
+}
+
+int flexq_linear_w4_exact(int M, int K, int group_size) {
+  if (M <= 0 || check_w4_shape(1, K, group_size)) return 0;
+  return gemv_takes(M, flexq::w4_col_tiles(K), log2_gs(group_size)) ? 1 : 0;
 }
 
 int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,

@@ -119,6 +119,7 @@ def lib():
             "flexq_weight4_packed_bytes": (c_size_t, [c_int, c_int, c_int]),
             "flexq_quantize_weight4": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p,
                                                c_void_p, c_void_p]),
+            "flexq_linear_w4_exact": (c_int, [c_int, c_int, c_int]),
             "flexq_linear_w4": (c_int, [c_int, c_int, c_int, c_int, c_int, c_void_p, c_ll,
                                         c_void_p, c_void_p, c_void_p, c_ll, c_void_p]),
             "flexq_linear_w4_group": (c_int, [c_int, c_int, c_int, c_int, c_void_p, c_ll, c_int,
@@ -615,6 +616,12 @@ def _w4_input(x):
     if not _is_rows(x, dtype, (M, K), dev):
         _refuse_rows(x, "x", dtype, (M, K), x)
     return dtype, dev, M, K, _row_stride(x, M, K)
+
+
+def linear4_exact(M, K, group_size):
+    """Whether linear4 multiplies the codes themselves for a batch of M tokens;
+    larger batches round the dequantized weights to x's type first."""
+    return bool(lib().flexq_linear_w4_exact(M, K, group_size))
 
 
 def linear4(x, wp, ws, N, group_size, out=None):

@@ -407,11 +407,12 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
  *   Y, ldy     out, [M, N], rows ldy >= N elements apart; nothing between the
  *              rows is written.  Y needs its elements' alignment only.
  * Y[m,n] = round(sum_g s[n,g] * sum_{k in g} X[m,k] q[n,k]), sums in FP32,
- * rounded once.  Batches of more than 16 tokens (and ones whose activations do
- * not fit an SM's shared memory) multiply weights that are rounded to dtype:
- * Y[m,n] = round(sum_k X[m,k] round(s[n,g] q[n,k])), infinite where 7 s
+ * rounded once, for batches of at most 16 tokens of moderate K
+ * (flexq_linear_w4_exact).  Larger ones multiply weights that are rounded to
+ * dtype: Y[m,n] = round(sum_k X[m,k] round(s[n,g] q[n,k])), infinite where 7 s
  * exceeds FP16's range.  The summation order depends on the shapes alone.
  */
+int flexq_linear_w4_exact(int M, int K, int group_size);
 int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,
                     const void* Wq_packed, const void* W_scales, void* Y, long long ldy,
                     void* stream);

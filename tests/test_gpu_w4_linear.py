@@ -28,12 +28,12 @@ def packed(w, gs):
     return wp, ws, dequantize(q, s)
 
 
-def check(y, x, w64, dtype, tokens=None):
+def check(y, x, w64, dtype, gs, tokens=None):
     x64, tokens = to64(x), x.shape[0] if tokens is None else tokens
     ref, mags = x64 @ w64.T, np.abs(x64) @ np.abs(w64).T
     tiles = -(-x64.shape[1] // 128)
     tol = (half_step(dtype) * np.abs(ref) + (48 + tiles) * 2.0 ** -23 * mags + 2.0 ** -25)
-    if tokens > 16:
+    if not flexq.linear4_exact(tokens, x64.shape[1], gs):
         tol += half_step(dtype) * mags + 2.0 ** -25 * np.abs(x64).sum(1, keepdims=True)
     bad = np.abs(to64(y) - ref) > tol
     assert not bad.any(), f"{bad.sum()} of {bad.size}, worst {np.abs(to64(y) - ref).max()}"
@@ -72,13 +72,14 @@ def test_quantizer_edge_values():
     (1, 1, 32, 32), (1, 100, 160, 32), (2, 16, 128, 128), (3, 257, 288, 32), (5, 33, 320, 64),
     (7, 48, 192, 64), (8, 1000, 1024, 128), (9, 65, 512, 256), (16, 31, 4096, 128),
     (17, 129, 768, 256), (31, 40, 2080, 32), (33, 77, 1088, 64), (64, 130, 1024, 256),
+    (12, 700, 7168, 32), (16, 2400, 32768, 32), (16, 1500, 17408, 128), (32, 2500, 8192, 64), (24, 400, 28672, 256),
     (70, 129, 640, 128), (130, 300, 1024, 64), (300, 515, 2304, 256), (1, 4096, 4096, 128)])
 def test_linear_against_64_bits(M, N, K, gs, dtype):
     wp, ws, w64 = packed(weights(N, K, 3 * N + K), gs)
     x = inputs.activations(M, K, seed=M).to(dtype)
     y = flexq.linear4(x.cuda(), wp, ws, N, gs)
     assert y.dtype == dtype and y.shape == (M, N)
-    check(y, x, w64, dtype)
+    check(y, x, w64, dtype, gs)
 
 
 @pytest.mark.parametrize("M", [1, 12, 200])
@@ -104,7 +105,7 @@ def test_grouped_layers(M):
     x = inputs.activations(M, K, seed=2)
     ys = flexq.linear4_group(x.cuda(), [(wp, ws, n) for (wp, ws, _), n in zip(layers, Ns)], gs)
     for y, (_, _, w64) in zip(ys, layers):
-        check(y, x, w64, torch.float16)
+        check(y, x, w64, torch.float16, gs)
 
 
 @pytest.mark.parametrize("M", [3, 20, 140])
@@ -118,7 +119,7 @@ def test_rows_of_wider_matrices(M):
     wide[:, 32:32 + K] = x
     out = torch.full((M, N + 9), 7.0, dtype=torch.float16, device="cuda")
     y = flexq.linear4(wide.cuda()[:, 32:32 + K], wp, ws, N, gs, out=out[:, 4:4 + N])
-    check(y, x, w64, torch.float16)
+    check(y, x, w64, torch.float16, gs)
     assert (out[:, :4] == 7).all() and (out[:, 4 + N:] == 7).all()
 
 
@@ -133,7 +134,7 @@ def test_special_values_stay_in_their_token(M):
     assert torch.isnan(y[2]).all()
     assert not torch.isfinite(y[4]).all()
     keep = [m for m in range(M) if m not in (2, 4)]
-    check(y[keep], x[keep], w64, torch.float16, tokens=M)
+    check(y[keep], x[keep], w64, torch.float16, gs, tokens=M)
 
 
 def test_no_tokens():
@@ -164,7 +165,7 @@ def test_repeats_captured_and_on_another_stream(M):
     x2 = inputs.activations(M, K, seed=77)
     x.copy_(x2)
     graph.replay()
-    check(out, x2, w64, torch.float16)
+    check(out, x2, w64, torch.float16, gs)
 
 
 def test_refusals_on_the_gpu():

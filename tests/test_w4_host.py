@@ -48,6 +48,14 @@ def test_the_packed_form_by_plain_index_arithmetic():
     assert np.array_equal(unpack4(b, N, K), q)
 
 
+def test_which_batches_multiply_the_codes_themselves(L):
+    for M, K, gs in [(1, 32, 32), (1, 28672, 128), (8, 28672, 32), (16, 28672, 128), (16, 8192, 64)]:
+        assert flexq.linear4_exact(M, K, gs)
+    for M, K, gs in [(17, 256, 128), (16, 65536, 128), (2048, 4096, 64), (0, 256, 128),
+                     (1, 200, 128), (1, 1 << 22, 128)]:
+        assert not flexq.linear4_exact(M, K, gs)
+
+
 def test_linear_refusals_before_any_launch(L):
     f = L.flexq_linear_w4
     ok = (4, 100, 256, 128, 0, FAKE, 256, FAKE, FAKE, FAKE, 100, NULL)

@@ -22,40 +22,53 @@ struct Table {
   int V, K, G, kbs, gs_shift;       // kbs: tiles of 128 columns, gs = 1 << gs_shift
 };
 
-// The word i (0..2) of 16-code block b (0..7) of a row of a 6-bit table.
-__device__ __forceinline__ uint32_t w6_block_word(const uint8_t* packed, int v, int kb, int kbs, int b,
-                                                  int i) {
-  const int o = 12 * b + 4 * i;
-  return __ldg(reinterpret_cast<const uint32_t*>(
-      packed + (static_cast<size_t>(v >> 7) * kbs + kb) * 12288 +
-      static_cast<size_t>((o >> 4) * 128 + (v & 127)) * 16 + (o & 15)));
-}
-
-// The codes of columns k .. k+7 (k % 8 == 0) of row v.
+// The packed codes of eight columns k .. k+7 (k % 8 == 0) of a row: one word of
+// the 4-bit form, or the three words of the 16-code block that holds them.
 template <int BITS>
-__device__ __forceinline__ void table_codes8(const Table& tb, int v, int k, int (&q)[8]) {
-  if (BITS == 4) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tb.packed + w4_word_offset(v, k, tb.kbs)));
+struct Codes8 {
+  uint32_t w[BITS == 4 ? 1 : 3];
+
+  __device__ __forceinline__ void load(const Table& tb, int v, int k) {
+    if (BITS == 4) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(tb.packed + w4_word_offset(v, k, tb.kbs)));
+    } else {
+      // a row's 96 bytes of 128 codes lie in 16-byte chunks 128 rows apart
+      const uint8_t* tile = tb.packed + (static_cast<size_t>(v >> 7) * tb.kbs + (k >> 7)) * 12288 + (v & 127) * 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = w4_code(w, i);
-  } else {
-    // byte t of word i holds code 4 i + t in bits [7:2] and bits [2i+1:2i] of
-    // code 12 + t in bits [1:0]
-    const int kb = k >> 7, b = (k >> 4) & 7;
-    uint32_t w[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) w[i] = w6_block_word(tb.packed, v, kb, tb.kbs, b, i);
-    const bool upper = k & 8;
-    const uint32_t first = upper ? w[2] : w[0];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      q[t] = static_cast<int8_t>(first >> (8 * t)) >> 2;
-      const uint32_t u = ((w[0] >> (8 * t)) & 3u) | ((w[1] >> (8 * t)) & 3u) << 2 | ((w[2] >> (8 * t)) & 3u) << 4;
-      const int last = static_cast<int>(u << 26) >> 26;
-      q[4 + t] = upper ? last : static_cast<int8_t>(w[1] >> (8 * t)) >> 2;
+      for (int i = 0; i < 3; ++i) {
+        const int o = 12 * ((k >> 4) & 7) + 4 * i;
+        w[BITS == 4 ? 0 : i] = __ldg(reinterpret_cast<const uint32_t*>(tile + (o >> 4) * 2048 + (o & 15)));
+      }
     }
   }
-}
+
+  // The codes as FP32.
+  __device__ __forceinline__ void get(int k, float (&q)[8]) const {
+    if (BITS == 4) {
+      uint32_t p[4];
+      Elem<__half>::codes(w[0], p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = Elem<__half>::unpack(p[i]);
+        q[2 * i] = f.x;
+        q[2 * i + 1] = f.y;
+      }
+    } else {
+      // byte t of word i holds code 4 i + t in bits [7:2] and bits [2i+1:2i] of
+      // code 12 + t in bits [1:0]
+      const uint32_t w0 = w[0], w1 = w[BITS == 4 ? 0 : 1], w2 = w[BITS == 4 ? 0 : 2];
+      const bool upper = k & 8;
+      const uint32_t first = upper ? w2 : w0;
+      const uint32_t last = (w0 & 0x03030303u) << 2 | (w1 & 0x03030303u) << 4 | (w2 & 0x03030303u) << 6;
+      const uint32_t second = upper ? last : w1;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        q[t] = static_cast<float>(static_cast<int8_t>(first >> (8 * t)) >> 2);
+        q[4 + t] = static_cast<float>(static_cast<int8_t>(second >> (8 * t)) >> 2);
+      }
+    }
+  }
+};
 
 template <int BITS>
 __device__ __forceinline__ size_t scale_index(const Table& tb, int v, int grp) {
@@ -70,30 +83,50 @@ __device__ __forceinline__ int token_row(const void* ids, int id_bytes, long lon
 }
 
 // ------------------------------------------------------------------ lookup --
-// One thread per eight columns of a token: consecutive threads write
-// consecutive 16-byte pieces of a row.
+// Bound by writing the rows: 16 bytes a thread, consecutive threads write
+// consecutive pieces.  A thread keeps its columns and takes kLookAhead tokens
+// at a time, so that their ids, then their codes and scales, are in flight
+// together.
+constexpr int kLookThreads = 256;
+constexpr int kLookCols = kLookThreads * 8;
+constexpr int kLookAhead = 4;
+
 template <typename T, int BITS>
-__global__ void __launch_bounds__(256) embed_kernel(const Table tb, const void* __restrict__ ids,
-                                                    int id_bytes, long long units, float scale,
-                                                    T* __restrict__ out) {
-  const int per_row = tb.K >> 3;
-  for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < units;
-       u += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const long long tok = u / per_row;
-    const int k = static_cast<int>(u - tok * per_row) * 8;
-    const int v = token_row(ids, id_bytes, tok, tb.V);
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (v >= 0) {
-      int q[8];
-      table_codes8<BITS>(tb, v, k, q);
-      const float s = __half2float(__ldg(tb.scales + scale_index<BITS>(tb, v, k >> tb.gs_shift)));
-      uint32_t* p = reinterpret_cast<uint32_t*>(&o);
+__global__ void __launch_bounds__(kLookThreads) embed_kernel(const Table tb, const void* __restrict__ ids,
+                                                             int id_bytes, int tokens, float scale,
+                                                             T* __restrict__ out) {
+  const int k = blockIdx.y * kLookCols + threadIdx.x * 8;
+  if (k >= tb.K) return;
+  const int grp = k >> tb.gs_shift;
+  for (long long t0 = static_cast<long long>(blockIdx.x) * kLookAhead; t0 < tokens;
+       t0 += static_cast<long long>(gridDim.x) * kLookAhead) {
+    int v[kLookAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)        // code * scale is exact in FP32
-        p[i] = Elem<T>::pack(static_cast<float>(q[2 * i]) * s * scale,
-                             static_cast<float>(q[2 * i + 1]) * s * scale);
+    for (int j = 0; j < kLookAhead; ++j)
+      v[j] = t0 + j < tokens ? token_row(ids, id_bytes, t0 + j, tb.V) : -1;
+    Codes8<BITS> c[kLookAhead];
+    __half s[kLookAhead];
+#pragma unroll
+    for (int j = 0; j < kLookAhead; ++j)
+      if (v[j] >= 0) {
+        c[j].load(tb, v[j], k);
+        s[j] = __ldg(tb.scales + scale_index<BITS>(tb, v[j], grp));
+      }
+#pragma unroll
+    for (int j = 0; j < kLookAhead; ++j) {
+      if (t0 + j >= tokens) break;
+      uint4 o = make_uint4(0, 0, 0, 0);
+      if (v[j] >= 0) {
+        float q[8];
+        c[j].get(k, q);
+        const float f = __half2float(s[j]);
+        uint32_t* p = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)      // code * scale is exact in FP32
+          p[i] = Elem<T>::pack(q[2 * i] * f * scale, q[2 * i + 1] * f * scale);
+      }
+      __stcs(reinterpret_cast<uint4*>(out + static_cast<size_t>(t0 + j) * tb.K + k), o);
     }
-    *reinterpret_cast<uint4*>(out + tok * tb.K + k) = o;
   }
 }
 
@@ -129,6 +162,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     const long long stride = static_cast<long long>(gridDim.x - C) * kSortThreads;
 #pragma unroll
     for (int f = 0; f < 2; ++f)
+#pragma unroll 4
       for (long long i = static_cast<long long>(blockIdx.x - C) * kSortThreads + threadIdx.x;
            i < a.fill_n[f]; i += stride)
         a.fill[f][i] = make_uint4(0, 0, 0, 0);
@@ -236,11 +270,12 @@ struct SumArgs {
   float* scales;                  // scale gradient, or null
 };
 
-// Writes the finished sums of columns k .. k+7 of row v.  All threads of a
-// warp take part (the group sums are shuffles); `in` says whose columns exist.
+// Writes the finished sums of columns k .. k+7 of row v; codes: the row's, where
+// the scales' gradient is wanted.  All threads of a warp take part (the group
+// sums are shuffled); `in` says whose columns exist.
 template <typename T, typename TO, int BITS>
 __device__ __forceinline__ void embed_finish(const Table& tb, const SumArgs& a, int v, int k, bool in,
-                                             const float (&acc)[8]) {
+                                             const float (&acc)[8], const Codes8<BITS>& codes) {
   float d[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) d[i] = acc[i] * a.scale;
@@ -261,10 +296,10 @@ __device__ __forceinline__ void embed_finish(const Table& tb, const SumArgs& a, 
   if (a.scales) {
     float sum = 0.0f;
     if (in) {
-      int q[8];
-      table_codes8<BITS>(tb, v, k, q);
+      float q[8];
+      codes.get(k, q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(d[i], static_cast<float>(q[i]), sum);
+      for (int i = 0; i < 8; ++i) sum = fmaf(d[i], q[i], sum);
     }
     const int lanes = 1 << (tb.gs_shift - 3);         // threads per group: 4 .. 32
     for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -288,7 +323,8 @@ __device__ __forceinline__ void add8(float (&acc)[8], const uint4& x) {
 // rows inside the tile are finished here; what a run has in a tile that it
 // shares with others goes to `partial` and is joined by embed_join_kernel, so
 // that a row with many tokens is spread over many CTAs and every sum has one
-// fixed order.
+// fixed order.  Bound by reading dY: eight rows of it, and the codes of the
+// rows that end among them, are in flight per thread.
 template <typename T, typename TO, int BITS>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, const SumArgs a) {
   __shared__ uint2 items[kSumMaxTile + 2];            // with the neighbours on both sides
@@ -302,25 +338,29 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, 
   const int k = blockIdx.y * kSumCols + threadIdx.x * 8;
   const bool in = k < tb.K;
   const T* dy = static_cast<const T*>(a.dy);
-  constexpr int kAhead = 8;                           // loads in flight per thread
+  const unsigned V = static_cast<unsigned>(tb.V);
+  constexpr int kAhead = 8;
   float acc[8] = {};
   for (int i0 = 0; i0 < n; i0 += kAhead) {
     uint4 x[kAhead];
+    Codes8<BITS> codes[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (in && i0 + j < n && items[1 + i0 + j].x < static_cast<unsigned>(tb.V))
-        x[j] = __ldcs(reinterpret_cast<const uint4*>(dy + static_cast<size_t>(items[1 + i0 + j].y) * tb.K + k));
+      if (in && i0 + j < n && items[1 + i0 + j].x < V) {
+        const uint2 it = items[1 + i0 + j];
+        x[j] = __ldcs(reinterpret_cast<const uint4*>(dy + static_cast<size_t>(it.y) * tb.K + k));
+        if (a.scales && items[2 + i0 + j].x != it.x) codes[j].load(tb, static_cast<int>(it.x), k);
+      }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j;
       if (i >= n) break;
       const unsigned v = items[1 + i].x;
-      if (v >= static_cast<unsigned>(tb.V)) return;   // padding sorts last
+      if (v >= V) return;                             // padding sorts last
       if (in) add8<T>(acc, x[j]);
       if (i + 1 < n && items[2 + i].x == v) continue; // the run goes on in this tile
-      const bool first_run = v == items[1].x;
-      const bool shared_before = first_run && items[0].x == v;
-      const bool shared_after = i + 1 == n && items[2 + i].x == v;
+      const bool shared_before = v == items[1].x && items[0].x == v;
+      const bool shared_after = items[2 + i].x == v;  // then i is the tile's last
       if (shared_before || shared_after) {
         if (in) {
           float4* p = reinterpret_cast<float4*>(
@@ -329,7 +369,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, 
           p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         }
       } else {
-        embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc);
+        embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc, codes[j]);
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
@@ -348,22 +388,149 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const Table tb,
   if (begin > 0 && a.sorted[begin].x == v && a.sorted[begin - 1].x == v) return;   // starts earlier
   const int k = blockIdx.y * kSumCols + threadIdx.x * 8;
   const bool in = k < tb.K;
+  Codes8<BITS> codes;
+  if (in && a.scales) codes.load(tb, static_cast<int>(v), k);
   float acc[8] = {};
-  auto add = [&](size_t slot) {
-    if (!in) return;
+  auto get = [&](size_t slot, float4 (&x)[2]) {
     const float4* p = reinterpret_cast<const float4*>(a.partial + slot * tb.K + k);
-    const float4 x = p[0], y = p[1];
-    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-    acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+    x[0] = p[0];
+    x[1] = p[1];
   };
-  size_t tile = blockIdx.x;
-  add(tile * 2 + 1);
-  for (long long e = end;; e += a.tile) {             // tiles that begin with v
-    ++tile;
-    add(tile * 2);
-    if (e + a.tile >= a.T || a.sorted[e + a.tile - 1].x != v || a.sorted[e + a.tile].x != v) break;
+  auto add = [&](const float4 (&x)[2]) {
+    acc[0] += x[0].x; acc[1] += x[0].y; acc[2] += x[0].z; acc[3] += x[0].w;
+    acc[4] += x[1].x; acc[5] += x[1].y; acc[6] += x[1].z; acc[7] += x[1].w;
+  };
+  if (in) {
+    float4 x[2];
+    get(static_cast<size_t>(blockIdx.x) * 2 + 1, x);
+    add(x);
   }
-  embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc);
+  // the tiles behind that begin with v: 32 of them are asked at once, and
+  // their parts come four at a time
+  const long long tiles = (static_cast<long long>(a.T) + a.tile - 1) / a.tile;
+  for (long long t0 = static_cast<long long>(blockIdx.x) + 1;; t0 += 32) {
+    const long long t = t0 + (threadIdx.x & 31);
+    const unsigned same = __ballot_sync(0xFFFFFFFFu, t < tiles && a.sorted[t * a.tile].x == v);
+    const int run = same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1;
+    if (in)
+      for (int i = 0; i < run; i += 4) {
+        float4 x[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < run) get(static_cast<size_t>(t0 + i + j) * 2, x[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < run) add(x[j]);
+      }
+    if (run < 32) break;
+  }
+  embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc, codes);
+}
+
+// ------------------------------------------------------------- few tokens ----
+// Up to 128 tokens take one launch: every CTA sorts them all by comparing each
+// with each (a microsecond, hidden behind nothing but cheaper than the three
+// launches above), then takes its share of the runs' 2048-column pieces, and of
+// the rows without a token, whose gradients it zeroes.
+constexpr int kFewTokens = 128;
+
+struct FewArgs {
+  SumArgs sum;
+  const void* ids;
+  int id_bytes;
+};
+
+template <typename T, typename TO, int BITS>
+__global__ void __launch_bounds__(kSumThreads) embed_few_kernel(const Table tb, const FewArgs f) {
+  const SumArgs& a = f.sum;
+  __shared__ int row_of[kFewTokens];                  // of each token; V for padding
+  __shared__ uint2 items[kFewTokens + 1];             // sorted
+  __shared__ int start[kFewTokens];                   // of each run, in the order of the rows
+  __shared__ int runs_of[kFewTokens / 32];
+  const int n = a.T, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < n) {
+    const int v = token_row(f.ids, f.id_bytes, tid, tb.V);
+    row_of[tid] = v < 0 ? tb.V : v;
+  }
+  __syncthreads();
+  if (tid < n) {
+    const int v = row_of[tid];
+    int at = 0;
+    for (int j = 0; j < n; ++j) at += row_of[j] < v || (row_of[j] == v && j < tid);
+    items[at] = make_uint2(static_cast<unsigned>(v), static_cast<unsigned>(tid));
+  }
+  if (tid == 0) items[n] = make_uint2(0xFFFFFFFFu, 0);
+  __syncthreads();
+  bool first = false;
+  unsigned here = 0;
+  if (warp < kFewTokens / 32) {
+    first = tid < n && items[tid].x < static_cast<unsigned>(tb.V) && (tid == 0 || items[tid - 1].x != items[tid].x);
+    here = __ballot_sync(0xFFFFFFFFu, first);
+    if (lane == 0) runs_of[warp] = __popc(here);
+  }
+  __syncthreads();
+  int runs = 0;
+  for (int w = 0; w < kFewTokens / 32; ++w) {
+    if (w == warp && first) start[runs + __popc(here & ((1u << lane) - 1u))] = tid;
+    runs += runs_of[w];
+  }
+  __syncthreads();
+
+  const int pieces = (tb.K + kSumCols - 1) / kSumCols;
+  const T* dy = static_cast<const T*>(a.dy);
+  for (int w = blockIdx.x; w < runs * pieces; w += gridDim.x) {
+    const int p = start[w / pieces], k = w % pieces * kSumCols + tid * 8;
+    const unsigned v = items[p].x;
+    const bool in = k < tb.K;
+    Codes8<BITS> codes;
+    if (in && a.scales) codes.load(tb, static_cast<int>(v), k);
+    float acc[8] = {};
+    constexpr int kAhead = 8;
+    for (int i0 = p; items[i0].x == v; i0 += kAhead) {
+      uint4 x[kAhead];
+      int m = 0;                                      // of them that belong to the run
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (m == j && i0 + j < n && items[i0 + j].x == v) {
+          if (in) x[j] = *reinterpret_cast<const uint4*>(dy + static_cast<size_t>(items[i0 + j].y) * tb.K + k);
+          m = j + 1;
+        }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (j < m && in) add8<T>(acc, x[j]);
+      if (m < kAhead || i0 + kAhead >= n) break;
+    }
+    embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc, codes);
+  }
+
+  // this CTA's share of the rows, less those of the runs
+  auto zero_rows = [&](int lo, int hi) {
+    if (a.table) {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<TO*>(a.table) + static_cast<size_t>(lo) * tb.K);
+      const long long m = static_cast<long long>(hi - lo) * tb.K * static_cast<int>(sizeof(TO)) / 16;
+      for (long long i = tid; i < m; i += kSumThreads) p[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (a.scales) {
+      if (BITS == 4) {
+        float* p = a.scales + static_cast<size_t>(lo) * tb.G;
+        const long long m = static_cast<long long>(hi - lo) * tb.G;
+        for (long long i = tid; i < m; i += kSumThreads) p[i] = 0.0f;
+      } else {
+        for (int g = warp; g < tb.G; g += kSumThreads / 32)
+          for (int v = lo + lane; v < hi; v += 32) a.scales[static_cast<size_t>(g) * tb.V + v] = 0.0f;
+      }
+    }
+  };
+  const int share_lo = static_cast<int>(static_cast<long long>(blockIdx.x) * tb.V / gridDim.x);
+  const int share_hi = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * tb.V / gridDim.x);
+  int lo = share_lo;
+  for (int r = 0; r <= runs && lo < share_hi; ++r) {
+    const int row = r < runs ? static_cast<int>(items[start[r]].x) : tb.V;
+    if (row < lo) continue;
+    const int hi = min(row, share_hi);
+    if (lo < hi) zero_rows(lo, hi);
+    lo = row + 1;
+  }
 }
 
 }  // namespace flexq

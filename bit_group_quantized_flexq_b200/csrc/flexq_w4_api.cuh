@@ -356,12 +356,12 @@ flexq::Table make_table(const void* Wq, const void* Ws, int V, int K, int gs) {
 }
 
 template <typename T>
-void launch_embed(int bits, const flexq::Table& tb, const void* ids, int id_bytes, long long units,
-                  float scale, void* out, unsigned grid, cudaStream_t s) {
+void launch_embed(int bits, const flexq::Table& tb, const void* ids, int id_bytes, int tokens,
+                  float scale, void* out, dim3 grid, cudaStream_t s) {
   if (bits == 4)
-    flexq::embed_kernel<T, 4><<<grid, 256, 0, s>>>(tb, ids, id_bytes, units, scale, static_cast<T*>(out));
+    flexq::embed_kernel<T, 4><<<grid, flexq::kLookThreads, 0, s>>>(tb, ids, id_bytes, tokens, scale, static_cast<T*>(out));
   else
-    flexq::embed_kernel<T, 6><<<grid, 256, 0, s>>>(tb, ids, id_bytes, units, scale, static_cast<T*>(out));
+    flexq::embed_kernel<T, 6><<<grid, flexq::kLookThreads, 0, s>>>(tb, ids, id_bytes, tokens, scale, static_cast<T*>(out));
 }
 
 // Sorted tokens per CTA: two CTAs per SM and column block where there are
@@ -375,10 +375,16 @@ int sum_tile(long long T, int K) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t backward_workspace(long long T, int K) {
-  if (T <= 0) return 0;
+  if (T <= flexq::kFewTokens) return 0;
   const long long tiles = (T + sum_tile(T, K) - 1) / sum_tile(T, K);
   return 2 * align256(static_cast<size_t>(T) * sizeof(uint2)) +
          static_cast<size_t>(tiles) * 2 * K * sizeof(float);
+}
+
+template <typename T, typename TO>
+void launch_few(int bits, const flexq::Table& tb, const flexq::FewArgs& f, unsigned grid, cudaStream_t s) {
+  if (bits == 4) flexq::embed_few_kernel<T, TO, 4><<<grid, flexq::kSumThreads, 0, s>>>(tb, f);
+  else flexq::embed_few_kernel<T, TO, 6><<<grid, flexq::kSumThreads, 0, s>>>(tb, f);
 }
 
 template <typename T, typename TO, int BITS>
@@ -458,13 +464,15 @@ int flexq_embedding(long long T, int V, int K, int group_size, int weight_bits, 
   DeviceState* st = nullptr;
   if ((rc = device_state(&st))) return rc;
   const flexq::Table tb = make_table(Wq_packed, W_scales, V, K, group_size);
-  const long long units = T * (K / 8);
-  const unsigned grid = static_cast<unsigned>(std::min<long long>((units + 255) / 256, 32LL * st->sms));
+  // a CTA's columns by tokens; up to 16 CTAs per SM take turns at the tokens
+  const unsigned cols = static_cast<unsigned>((K + flexq::kLookCols - 1) / flexq::kLookCols);
+  const long long turns = (T + flexq::kLookAhead - 1) / flexq::kLookAhead;
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(turns, std::max(1LL, 16LL * st->sms / cols))), cols);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == FLEXQ_DTYPE_FP16)
-    launch_embed<__half>(weight_bits, tb, ids, id_bytes, units, scale, out, grid, s);
+    launch_embed<__half>(weight_bits, tb, ids, id_bytes, static_cast<int>(T), scale, out, grid, s);
   else
-    launch_embed<__nv_bfloat16>(weight_bits, tb, ids, id_bytes, units, scale, out, grid, s);
+    launch_embed<__nv_bfloat16>(weight_bits, tb, ids, id_bytes, static_cast<int>(T), scale, out, grid, s);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "embedding launch");
   return ok();
@@ -490,7 +498,7 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
   if (T > 0) {
     const void* ptrs[] = {dY, workspace};
     const char* names[] = {"dY", "workspace"};
-    if ((rc = check_ptrs(2, ptrs, names))) return rc;
+    if ((rc = check_ptrs(need ? 2 : 1, ptrs, names))) return rc;
     if (!ids) return fail(FLEXQ_ERR_INVALID_ARG, "ids is NULL");
     if (reinterpret_cast<uintptr_t>(ids) % static_cast<unsigned>(id_bytes))
       return fail(FLEXQ_ERR_MISALIGNED, "ids is not %d-byte aligned", id_bytes);
@@ -506,6 +514,27 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
   if ((rc = device_state(&st))) return rc;
 
   const flexq::Table tb = make_table(Wq_packed, nullptr, V, K, group_size);
+  const bool wide = d_table && table_dtype == FLEXQ_DTYPE_FP32;
+  flexq::SumArgs a = {};
+  a.dy = dY;
+  a.T = static_cast<int>(T);
+  a.scale = scale;
+  a.table = d_table;
+  a.scales = d_scales;
+  if (T <= flexq::kFewTokens) {
+    const flexq::FewArgs f = {a, ids, id_bytes};
+    const unsigned grid = static_cast<unsigned>(std::min(V, 4 * st->sms));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == FLEXQ_DTYPE_FP16) {
+      if (wide) launch_few<__half, float>(weight_bits, tb, f, grid, s);
+      else launch_few<__half, __half>(weight_bits, tb, f, grid, s);
+    } else {
+      if (wide) launch_few<__nv_bfloat16, float>(weight_bits, tb, f, grid, s);
+      else launch_few<__nv_bfloat16, __nv_bfloat16>(weight_bits, tb, f, grid, s);
+    }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ok() : cuda_fail(e, "embedding gradient launch");
+  }
   const size_t item_bytes = align256(static_cast<size_t>(T) * sizeof(uint2));
   char* ws = static_cast<char*>(workspace);
   flexq::SortArgs so = {};
@@ -515,7 +544,7 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
   so.V = V;
   for (so.passes = 1; so.passes < 4 && (static_cast<long long>(V) >> (8 * so.passes)); ++so.passes) {}
   so.buf[0] = reinterpret_cast<uint2*>(ws);
-  so.buf[1] = reinterpret_cast<uint2*>(ws + (T > 0 ? item_bytes : 0));
+  so.buf[1] = reinterpret_cast<uint2*>(ws + item_bytes);
   const size_t table_bytes =
       d_table ? static_cast<size_t>(V) * K * (table_dtype == FLEXQ_DTYPE_FP32 ? 4 : 2) : 0;
   const size_t scale_elems = d_scales ? static_cast<size_t>(V) * (K / group_size) : 0;
@@ -542,18 +571,10 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
   cfg.numAttrs = C > 1 ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, flexq::embed_sort_kernel, so);
   if (e != cudaSuccess) return cuda_fail(e, "token sort launch");
-  if (T == 0) return ok();
 
-  flexq::SumArgs a = {};
   a.sorted = so.buf[(so.passes - 1) & 1];
-  a.dy = dY;
-  a.T = so.T;
   a.tile = sum_tile(T, K);
-  a.scale = scale;
   a.partial = reinterpret_cast<float*>(ws + 2 * item_bytes);
-  a.table = d_table;
-  a.scales = d_scales;
-  const bool wide = d_table && table_dtype == FLEXQ_DTYPE_FP32;
   if (dtype == FLEXQ_DTYPE_FP16) {
     if (wide) launch_sums_bits<__half, float>(weight_bits, tb, a, cfg.stream);
     else launch_sums_bits<__half, __half>(weight_bits, tb, a, cfg.stream);

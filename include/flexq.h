@@ -448,8 +448,8 @@ int flexq_embedding(long long T, int V, int K, int group_size, int weight_bits, 
                     const void* ids, int id_bytes, const void* Wq_packed, const void* W_scales,
                     float scale, void* out, void* stream);
 
-/* Device scratch of flexq_embedding_backward (need not be cleared; 0 for
- * T <= 0). */
+/* Device scratch of flexq_embedding_backward (need not be cleared; 0 for few
+ * tokens, where workspace may be NULL). */
 size_t flexq_embedding_backward_workspace_bytes(long long T, int K);
 
 /*

@@ -22,24 +22,41 @@ struct Table {
   int V, K, G, kbs, gs_shift;       // kbs: tiles of 128 columns, gs = 1 << gs_shift
 };
 
+// Where a row's codes begin in a table.
+template <int BITS>
+__device__ __forceinline__ size_t row_offset(const Table& tb, int v) {
+  return BITS == 4 ? static_cast<size_t>(v >> 4) * tb.kbs * kW4TileBytes + (v & 15) * 64
+                   : static_cast<size_t>(v >> 7) * tb.kbs * 12288 + (v & 127) * 16;
+}
+
 // The packed codes of eight columns k .. k+7 (k % 8 == 0) of a row: one word of
 // the 4-bit form, or the three words of the 16-code block that holds them.
 template <int BITS>
 struct Codes8 {
-  uint32_t w[BITS == 4 ? 1 : 3];
+  static constexpr int kWords = BITS == 4 ? 1 : 3;
+  uint32_t w[kWords];
 
-  __device__ __forceinline__ void load(const Table& tb, int v, int k) {
+  // The words' places from the row's beginning.
+  static __device__ __forceinline__ void places(int k, uint32_t (&at)[kWords]) {
     if (BITS == 4) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(tb.packed + w4_word_offset(v, k, tb.kbs)));
+      at[0] = static_cast<uint32_t>(k >> 7) * kW4TileBytes + ((k >> 3) & 3) * 16 + ((k >> 5) & 3) * 4;
     } else {
       // a row's 96 bytes of 128 codes lie in 16-byte chunks 128 rows apart
-      const uint8_t* tile = tb.packed + (static_cast<size_t>(v >> 7) * tb.kbs + (k >> 7)) * 12288 + (v & 127) * 16;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
+      for (int i = 0; i < kWords; ++i) {
         const int o = 12 * ((k >> 4) & 7) + 4 * i;
-        w[BITS == 4 ? 0 : i] = __ldg(reinterpret_cast<const uint32_t*>(tile + (o >> 4) * 2048 + (o & 15)));
+        at[i] = static_cast<uint32_t>(k >> 7) * 12288 + (o >> 4) * 2048 + (o & 15);
       }
     }
+  }
+  __device__ __forceinline__ void load(const uint8_t* row, const uint32_t (&at)[kWords]) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + at[i]));
+  }
+  __device__ __forceinline__ void load(const Table& tb, int v, int k) {
+    uint32_t at[kWords];
+    places(k, at);
+    load(tb.packed + row_offset<BITS>(tb, v), at);
   }
 
   // The codes as FP32.
@@ -56,7 +73,7 @@ struct Codes8 {
     } else {
       // byte t of word i holds code 4 i + t in bits [7:2] and bits [2i+1:2i] of
       // code 12 + t in bits [1:0]
-      const uint32_t w0 = w[0], w1 = w[BITS == 4 ? 0 : 1], w2 = w[BITS == 4 ? 0 : 2];
+      const uint32_t w0 = w[0], w1 = w[kWords / 2], w2 = w[kWords - 1];
       const bool upper = k & 8;
       const uint32_t first = upper ? w2 : w0;
       const uint32_t last = (w0 & 0x03030303u) << 2 | (w1 & 0x03030303u) << 4 | (w2 & 0x03030303u) << 6;
@@ -276,10 +293,10 @@ struct SumArgs {
 template <typename T, typename TO, int BITS>
 __device__ __forceinline__ void embed_finish(const Table& tb, const SumArgs& a, int v, int k, bool in,
                                              const float (&acc)[8], const Codes8<BITS>& codes) {
-  float d[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) d[i] = acc[i] * a.scale;
   if (a.table && in) {
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = acc[i] * a.scale;
     TO* row = static_cast<TO*>(a.table) + static_cast<size_t>(v) * tb.K + k;
     if constexpr (sizeof(TO) == 4) {
       reinterpret_cast<float4*>(row)[0] = make_float4(d[0], d[1], d[2], d[3]);
@@ -299,82 +316,148 @@ __device__ __forceinline__ void embed_finish(const Table& tb, const SumArgs& a, 
       float q[8];
       codes.get(k, q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(d[i], q[i], sum);
+      for (int i = 0; i < 8; ++i) sum = fmaf(acc[i], q[i], sum);
     }
-    const int lanes = 1 << (tb.gs_shift - 3);         // threads per group: 4 .. 32
-    for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    // gs / 8 threads per group: 4 .. 32
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+    if (tb.gs_shift > 5) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+    if (tb.gs_shift > 6) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+    if (tb.gs_shift > 7) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
     if (in && (k & ((1 << tb.gs_shift) - 1)) == 0)
-      a.scales[scale_index<BITS>(tb, v, k >> tb.gs_shift)] = sum;
+      a.scales[scale_index<BITS>(tb, v, k >> tb.gs_shift)] = sum * a.scale;
   }
 }
 
 template <typename T>
 __device__ __forceinline__ void add8(float (&acc)[8], const uint4& x) {
   const uint32_t* p = reinterpret_cast<const uint32_t*>(&x);
+  float2* a = reinterpret_cast<float2*>(acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = Elem<T>::unpack(p[i]);
-    acc[2 * i] += f.x;
-    acc[2 * i + 1] += f.y;
-  }
+  for (int i = 0; i < 4; ++i) a[i] = __fadd2_rn(a[i], Elem<T>::unpack(p[i]));
 }
 
-// One CTA: a tile of consecutive sorted tokens, 2048 columns.  Runs of equal
+// Copies into shared memory that the copying thread alone reads: it waits for
+// its own groups of them.
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One CTA: a tile of consecutive sorted tokens, 4096 columns.  Runs of equal
 // rows inside the tile are finished here; what a run has in a tile that it
 // shares with others goes to `partial` and is joined by embed_join_kernel, so
 // that a row with many tokens is spread over many CTAs and every sum has one
-// fixed order.  Bound by reading dY: eight rows of it, and the codes of the
-// rows that end among them, are in flight per thread.
+// fixed order.  Bound by reading dY: a thread takes two pieces of eight
+// columns, 2048 apart, and keeps six tokens' values (and the codes of the rows
+// that end with them) on the way into shared memory; what there is to know of
+// a token is worked out once per tile.  (With the values on the way to
+// registers instead, a wait for one token's waited for the next ones' too:
+// 16384 tokens x 8192 took 100 us.)
+template <int BITS>
+struct SumRing {
+  static constexpr int kStages = 6;
+  uint4 x[kStages][2][kSumThreads];
+  uint32_t codes[kStages][2][Codes8<BITS>::kWords][kSumThreads];
+};
+
 template <typename T, typename TO, int BITS>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, const SumArgs a) {
-  __shared__ uint2 items[kSumMaxTile + 2];            // with the neighbours on both sides
+  enum { kGoOn, kFinish, kBegun, kOpen };             // what follows a token's values
+  struct __align__(16) Item {
+    const T* dy;                                      // its values
+    const uint8_t* codes;                             // its row's
+    int row, next;
+  };
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  SumRing<BITS>& ring = *reinterpret_cast<SumRing<BITS>*>(ring_mem);
+  constexpr int D = SumRing<BITS>::kStages;
+  __shared__ Item items[kSumMaxTile];
+  __shared__ int valid;
+  const int tid = threadIdx.x;
   const long long p0 = static_cast<long long>(blockIdx.x) * a.tile;
-  const int n = static_cast<int>(min(static_cast<long long>(a.tile), a.T - p0));
-  for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
-    const long long p = p0 + i - 1;
-    items[i] = p >= 0 && p < a.T ? a.sorted[p] : make_uint2(0xFFFFFFFFu, 0);
-  }
+  if (tid == 0) valid = 0;
   __syncthreads();
-  const int k = blockIdx.y * kSumCols + threadIdx.x * 8;
-  const bool in = k < tb.K;
-  const T* dy = static_cast<const T*>(a.dy);
-  const unsigned V = static_cast<unsigned>(tb.V);
-  constexpr int kAhead = 8;
-  float acc[8] = {};
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
-    uint4 x[kAhead];
-    Codes8<BITS> codes[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (in && i0 + j < n && items[1 + i0 + j].x < V) {
-        const uint2 it = items[1 + i0 + j];
-        x[j] = __ldcs(reinterpret_cast<const uint4*>(dy + static_cast<size_t>(it.y) * tb.K + k));
-        if (a.scales && items[2 + i0 + j].x != it.x) codes[j].load(tb, static_cast<int>(it.x), k);
-      }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j;
-      if (i >= n) break;
-      const unsigned v = items[1 + i].x;
-      if (v >= V) return;                             // padding sorts last
-      if (in) add8<T>(acc, x[j]);
-      if (i + 1 < n && items[2 + i].x == v) continue; // the run goes on in this tile
-      const bool shared_before = v == items[1].x && items[0].x == v;
-      const bool shared_after = items[2 + i].x == v;  // then i is the tile's last
-      if (shared_before || shared_after) {
-        if (in) {
-          float4* p = reinterpret_cast<float4*>(
-              a.partial + (static_cast<size_t>(blockIdx.x) * 2 + (shared_before ? 0 : 1)) * tb.K + k);
-          p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        }
-      } else {
-        embed_finish<T, TO, BITS>(tb, a, static_cast<int>(v), k, in, acc, codes[j]);
-      }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+  if (tid < a.tile && p0 + tid < a.T) {
+    const long long p = p0 + tid, end = min(p0 + a.tile, static_cast<long long>(a.T));
+    const uint2 it = a.sorted[p];
+    if (it.x < static_cast<unsigned>(tb.V)) {         // padding sorts last
+      const unsigned behind = p + 1 < a.T ? a.sorted[p + 1].x : 0xFFFFFFFFu;
+      const bool begun = p0 > 0 && a.sorted[p0 - 1].x == it.x;
+      Item item;
+      item.dy = static_cast<const T*>(a.dy) + static_cast<size_t>(it.y) * tb.K;
+      item.codes = tb.packed + row_offset<BITS>(tb, static_cast<int>(it.x));
+      item.row = static_cast<int>(it.x);
+      item.next = behind == it.x && p + 1 < end ? kGoOn : begun ? kBegun : behind == it.x ? kOpen : kFinish;
+      items[tid] = item;
+      atomicMax(&valid, tid + 1);
     }
   }
+  __syncthreads();
+  const int n = valid;
+  const int k0 = blockIdx.y * (2 * kSumCols) + tid * 8;
+  uint32_t at[2][Codes8<BITS>::kWords];
+  Codes8<BITS>::places(k0, at[0]);
+  Codes8<BITS>::places(k0 + kSumCols, at[1]);
+  auto request = [&](int i, int slot) {
+    if (i < n) {
+      const Item& it = items[i];
+      const bool codes = a.scales && it.next == kFinish;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = k0 + u * kSumCols;
+        if (k < tb.K) {
+          async_copy16(smem_u32(&ring.x[slot][u][tid]), it.dy + k);
+          if (codes)
+#pragma unroll
+            for (int w = 0; w < Codes8<BITS>::kWords; ++w)
+              async_copy4(smem_u32(&ring.codes[slot][u][w][tid]), it.codes + at[u][w]);
+        }
+      }
+    }
+    async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) request(i, i);
+  float acc[2][8] = {};
+  int slot = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    async_wait<D - 1>();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (k0 + u * kSumCols < tb.K) add8<T>(acc[u], ring.x[slot][u][tid]);
+    const int next = items[i].next;
+    if (next != kGoOn) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = k0 + u * kSumCols;
+        if (next == kFinish) {
+          Codes8<BITS> codes;
+#pragma unroll
+          for (int w = 0; w < Codes8<BITS>::kWords; ++w) codes.w[w] = ring.codes[slot][u][w][tid];
+          embed_finish<T, TO, BITS>(tb, a, items[i].row, k, k < tb.K, acc[u], codes);
+        } else if (k < tb.K) {
+          float4* p = reinterpret_cast<float4*>(
+              a.partial + (static_cast<size_t>(blockIdx.x) * 2 + (next == kOpen ? 1 : 0)) * tb.K + k);
+          p[0] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+          p[1] = make_float4(acc[u][4], acc[u][5], acc[u][6], acc[u][7]);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[u][c] = 0.0f;
+      }
+    }
+    request(i + D, slot);
+    if (++slot == D) slot = 0;
+  }
+  async_wait<0>();
 }
 
 // Joins the run that starts in tile blockIdx.x and goes on into the next.
@@ -406,20 +489,20 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const Table tb,
     add(x);
   }
   // the tiles behind that begin with v: 32 of them are asked at once, and
-  // their parts come four at a time
+  // their parts come eight at a time
   const long long tiles = (static_cast<long long>(a.T) + a.tile - 1) / a.tile;
   for (long long t0 = static_cast<long long>(blockIdx.x) + 1;; t0 += 32) {
     const long long t = t0 + (threadIdx.x & 31);
     const unsigned same = __ballot_sync(0xFFFFFFFFu, t < tiles && a.sorted[t * a.tile].x == v);
     const int run = same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1;
     if (in)
-      for (int i = 0; i < run; i += 4) {
-        float4 x[4][2];
+      for (int i = 0; i < run; i += 8) {
+        float4 x[8][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 8; ++j)
           if (i + j < run) get(static_cast<size_t>(t0 + i + j) * 2, x[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 8; ++j)
           if (i + j < run) add(x[j]);
       }
     if (run < 32) break;

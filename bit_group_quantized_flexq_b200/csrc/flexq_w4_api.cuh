@@ -364,12 +364,13 @@ void launch_embed(int bits, const flexq::Table& tb, const void* ids, int id_byte
     flexq::embed_kernel<T, 6><<<grid, flexq::kLookThreads, 0, s>>>(tb, ids, id_bytes, tokens, scale, static_cast<T*>(out));
 }
 
-// Sorted tokens per CTA: two CTAs per SM and column block where there are
-// that many tokens, between 4 (a tile's overhead) and kSumMaxTile.
+// Sorted tokens per CTA: about six CTAs per SM where there are that many
+// tokens, between 16 (below, runs that several tiles share cost more than the
+// CTAs bring) and kSumMaxTile.
 int sum_tile(long long T, int K) {
-  const long long cols = (K + flexq::kSumCols - 1) / flexq::kSumCols;
-  const long long tile = T * cols / (2 * 148 * 2);
-  return static_cast<int>(std::max<long long>(4, std::min<long long>(flexq::kSumMaxTile, tile)));
+  const long long cols = (K + 2 * flexq::kSumCols - 1) / (2 * flexq::kSumCols);
+  const long long tile = T * cols / (6 * 148);
+  return static_cast<int>(std::max<long long>(16, std::min<long long>(flexq::kSumMaxTile, tile)));
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -388,17 +389,21 @@ void launch_few(int bits, const flexq::Table& tb, const flexq::FewArgs& f, unsig
 }
 
 template <typename T, typename TO, int BITS>
-void launch_sums(const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.T + static_cast<long long>(a.tile) - 1) / a.tile),
-                  static_cast<unsigned>((tb.K + flexq::kSumCols - 1) / flexq::kSumCols));
-  flexq::embed_sum_kernel<T, TO, BITS><<<grid, flexq::kSumThreads, 0, s>>>(tb, a);
-  if (grid.x > 1) flexq::embed_join_kernel<T, TO, BITS><<<grid, flexq::kSumThreads, 0, s>>>(tb, a);
+cudaError_t launch_sums(const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
+  static bool ready[kMaxDevices];
+  constexpr int smem = static_cast<int>(sizeof(flexq::SumRing<BITS>));
+  const cudaError_t e = allow_smem(flexq::embed_sum_kernel<T, TO, BITS>, smem, ready);
+  if (e != cudaSuccess) return e;
+  const unsigned tiles = static_cast<unsigned>((a.T + static_cast<long long>(a.tile) - 1) / a.tile);
+  const unsigned pieces = static_cast<unsigned>((tb.K + flexq::kSumCols - 1) / flexq::kSumCols);
+  flexq::embed_sum_kernel<T, TO, BITS><<<dim3(tiles, (pieces + 1) / 2), flexq::kSumThreads, smem, s>>>(tb, a);
+  if (tiles > 1) flexq::embed_join_kernel<T, TO, BITS><<<dim3(tiles, pieces), flexq::kSumThreads, 0, s>>>(tb, a);
+  return cudaGetLastError();
 }
 
 template <typename T, typename TO>
-void launch_sums_bits(int bits, const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
-  if (bits == 4) launch_sums<T, TO, 4>(tb, a, s);
-  else launch_sums<T, TO, 6>(tb, a, s);
+cudaError_t launch_sums_bits(int bits, const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
+  return bits == 4 ? launch_sums<T, TO, 4>(tb, a, s) : launch_sums<T, TO, 6>(tb, a, s);
 }
 
 }  // namespace
@@ -575,14 +580,12 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
   a.sorted = so.buf[(so.passes - 1) & 1];
   a.tile = sum_tile(T, K);
   a.partial = reinterpret_cast<float*>(ws + 2 * item_bytes);
-  if (dtype == FLEXQ_DTYPE_FP16) {
-    if (wide) launch_sums_bits<__half, float>(weight_bits, tb, a, cfg.stream);
-    else launch_sums_bits<__half, __half>(weight_bits, tb, a, cfg.stream);
-  } else {
-    if (wide) launch_sums_bits<__nv_bfloat16, float>(weight_bits, tb, a, cfg.stream);
-    else launch_sums_bits<__nv_bfloat16, __nv_bfloat16>(weight_bits, tb, a, cfg.stream);
-  }
-  e = cudaGetLastError();
+  if (dtype == FLEXQ_DTYPE_FP16)
+    e = wide ? launch_sums_bits<__half, float>(weight_bits, tb, a, cfg.stream)
+             : launch_sums_bits<__half, __half>(weight_bits, tb, a, cfg.stream);
+  else
+    e = wide ? launch_sums_bits<__nv_bfloat16, float>(weight_bits, tb, a, cfg.stream)
+             : launch_sums_bits<__nv_bfloat16, __nv_bfloat16>(weight_bits, tb, a, cfg.stream);
   if (e != cudaSuccess) return cuda_fail(e, "embedding gradient launch");
   return ok();
 }

@@ -39,14 +39,14 @@ constexpr int gemv_smem_limit(int M) {
 
 // Lets a kernel use more than 48 KB of shared memory, once per device.
 template <typename Kernel>
-cudaError_t allow_smem(Kernel kern, int bytes, bool (&done)[kMaxDevices]) {
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<unsigned long long>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(g_dev_mutex);
-  if (done[dev]) return cudaSuccess;
+  static_assert(kMaxDevices <= 64, "a bit per device");
+  if (done.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  done[dev] = e == cudaSuccess;
+  if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
   return e;
 }
 
@@ -134,9 +134,8 @@ bool gemv_plan(const flexq::W4Args& a, int strips, const int (&clusters)[4], Gem
 
 template <typename T, int WPG, int NT>
 int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, int sms, cudaStream_t stream) {
-  static bool ready[2][kMaxDevices];
-  cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT, false>, gemv_smem_limit(8 * NT), ready[0]);
-  if (e == cudaSuccess) e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT, true>, gemv_smem_limit(8 * NT), ready[1]);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT, false>, gemv_smem_limit(8 * NT), ready);
   const int (*clusters)[4] = nullptr;
   if (e == cudaSuccess) e = gemv_clusters<T, WPG, NT>(sms, clusters);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit linear set-up");
@@ -145,6 +144,11 @@ int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, int sms, cudaStream_t
     return fail(FLEXQ_ERR_UNSUPPORTED, "no launch for %d tokens, %d strips, K=%d", a.M, L.strip0[L.n], a.K);
   a.split = p.split;
   a.rounds = p.rounds;
+  if (p.rounds > 1) {
+    static std::atomic<unsigned long long> many{0};
+    e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT, true>, gemv_smem_limit(8 * NT), many);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit linear set-up");
+  }
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(static_cast<unsigned>(p.clusters * p.split), p.split,
                                                          static_cast<size_t>(p.smem), attr, stream);
@@ -211,7 +215,7 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
                   cudaStream_t stream) {
   using Cfg = flexq::W4MmaCfg<T, RB>;
   constexpr int dtype = std::is_same<E, __half>::value ? FLEXQ_DTYPE_FP16 : FLEXQ_DTYPE_BF16;
-  static bool ready[kMaxDevices];
+  static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem(flexq::w4_mma_kernel<E, T, RB>, Cfg::kSmem, ready);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   int rc = encode_w4_x_map(&a.x, x, dtype, a.M, a.K, ldx, T);
@@ -390,7 +394,7 @@ void launch_few(int bits, const flexq::Table& tb, const flexq::FewArgs& f, unsig
 
 template <typename T, typename TO, int BITS>
 cudaError_t launch_sums(const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
-  static bool ready[kMaxDevices];
+  static std::atomic<unsigned long long> ready{0};
   constexpr int smem = static_cast<int>(sizeof(flexq::SumRing<BITS>));
   const cudaError_t e = allow_smem(flexq::embed_sum_kernel<T, TO, BITS>, smem, ready);
   if (e != cudaSuccess) return e;

@@ -501,11 +501,14 @@ def linear_group(x, weights, group_size, act_bits=6, outs=None, workspace_buf=No
 # word a refusal.
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _LAYER4 = struct.Struct("@i4xPPPq").pack     # flexq_layer4_t
+_Tensor, _raw_stream, _cur_device = (torch.Tensor, torch._C._cuda_getCurrentRawStream,
+                                     torch._C._cuda_getDevice) if torch.cuda.is_available() else \
+    (torch.Tensor, None, None)
 
 
 def _is(t, dtype, shape, dev):
     """A contiguous tensor of this type and shape on CUDA device `dev`."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    return (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == dev and t.is_contiguous())
 
 
@@ -516,7 +519,7 @@ def _refuse(t, name, dtype, shape, like):
 
 def _is_rows(t, dtype, shape, dev):
     """The same of a matrix whose rows are contiguous but may lie apart."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    return (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == dev and (t.is_contiguous() or shape[1] <= 1 or t.stride(1) == 1))
 
 
@@ -541,23 +544,23 @@ def _row_stride(t, rows, cols):
 
 def _activation(t, name):
     """(type, CUDA device index) of an FP16 or BF16 tensor."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    dtype = t.dtype
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    return t.dtype, t.get_device()
+    return dtype, t.get_device()
 
 
 def _launch(dev, fn, *args):
     """fn(*args, current stream of `dev`) with `dev` as the current device."""
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch._C._cuda_getDevice():
-        status = fn(*args, stream)
+    if dev == _cur_device():
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, stream)
+            status = fn(*args, _raw_stream(dev))
     if status != FLEXQ_OK:
         _check(status)
 
@@ -594,6 +597,19 @@ def quantize_weight4(w, group_size, out=None):
     return wp, ws
 
 
+def _w4_input(x):
+    """(type code, type, device index, M, K, distance of the rows) of x."""
+    dtype, dev = _activation(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
+    M, K = x.shape
+    if x.is_contiguous():
+        return _DTYPES[dtype], dtype, dev, M, K, K
+    if not _is_rows(x, dtype, (M, K), dev):
+        _refuse_rows(x, "x", dtype, (M, K), x)
+    return _DTYPES[dtype], dtype, dev, M, K, _row_stride(x, M, K)
+
+
 def _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out):
     """The checked output of a layer, and the distance of its rows."""
     nbytes = _w4_bytes(N, K, group_size, "weight")
@@ -608,16 +624,6 @@ def _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out):
     return out, _row_stride(out, M, N)
 
 
-def _w4_input(x):
-    dtype, dev = _activation(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
-    M, K = x.shape
-    if not _is_rows(x, dtype, (M, K), dev):
-        _refuse_rows(x, "x", dtype, (M, K), x)
-    return dtype, dev, M, K, _row_stride(x, M, K)
-
-
 def linear4_exact(M, K, group_size):
     """Whether linear4 multiplies the codes themselves for a batch of M tokens;
     larger batches round the dequantized weights to x's type first."""
@@ -629,9 +635,9 @@ def linear4(x, wp, ws, N, group_size, out=None):
     BF16 activations x [M, K], which are not quantized; Y has x's type.  x and
     out may be views whose rows lie further apart (x: by a multiple of eight
     elements)."""
-    dtype, dev, M, K, ldx = _w4_input(x)
+    code, dtype, dev, M, K, ldx = _w4_input(x)
     y, ldy = _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out)
-    _launch(dev, lib().flexq_linear_w4, M, N, K, group_size, _DTYPES[dtype], x.data_ptr(), ldx,
+    _launch(dev, lib().flexq_linear_w4, M, N, K, group_size, code, x.data_ptr(), ldx,
             wp.data_ptr(), ws.data_ptr(), y.data_ptr(), ldy)
     return y
 
@@ -639,7 +645,7 @@ def linear4(x, wp, ws, N, group_size, out=None):
 def linear4_group(x, weights, group_size, outs=None):
     """Layers [(wp, ws, N), ...] with 4-bit weights that read the same
     activations x [M, K] (1..4 layers), in one launch; returns their outputs."""
-    dtype, dev, M, K, ldx = _w4_input(x)
+    code, dtype, dev, M, K, ldx = _w4_input(x)
     if not 1 <= len(weights) <= MAX_GROUP_LAYERS:
         raise ValueError(f"1..{MAX_GROUP_LAYERS} layers, got {len(weights)}")
     if outs is not None and len(outs) != len(weights):
@@ -650,7 +656,7 @@ def linear4_group(x, weights, group_size, outs=None):
                            None if outs is None else outs[i])
         layers += _LAYER4(N, wp.data_ptr(), ws.data_ptr(), y.data_ptr(), ldy)
         ys.append(y)
-    _launch(dev, lib().flexq_linear_w4_group, M, K, group_size, _DTYPES[dtype], x.data_ptr(), ldx,
+    _launch(dev, lib().flexq_linear_w4_group, M, K, group_size, code, x.data_ptr(), ldx,
             len(weights), layers)
     return ys
 

@@ -34,6 +34,14 @@ Configuration (a dict, or a JSON file holding one):
      "act_bits": {"q": 6, "k": 6, "v": 6, "o": 6, "gate": 6, "up": 6, "down": 8}}
 
 Every layer of the stack must be named, with 6 or 8 bits.
+
+Layers may keep 4-bit weights instead ("weight_bits", 6 where a layer is not
+named); their activations stay FP16, which "act_bits" says as 16:
+
+    {"group_size": 128, "weight_bits": {"gate": 4, "up": 4},
+     "act_bits": {"q": 6, "k": 6, "v": 6, "o": 6, "gate": 16, "up": 16, "down": 8}}
+
+They run through flexq.linear4_group, the layers of a site as one launch.
 """
 
 import json
@@ -51,14 +59,35 @@ LLAMA2_70B_MIXED = {
 }
 
 
-def parse_config(cfg, layers):
-    """(group size, {layer name: activation bits}) from a config dict or the
-    path of a JSON file; raises ValueError on anything missing or invalid."""
+def _load(cfg):
     if isinstance(cfg, (str, os.PathLike)):
         with open(cfg) as f:
             cfg = json.load(f)
     if not isinstance(cfg, dict):
         raise ValueError("config must be a dict or a JSON file holding one")
+    return cfg
+
+
+def parse_weight_bits(cfg, layers):
+    """{layer name: weight bits, 4 or 6} from a config dict or the path of a
+    JSON file; raises ValueError on anything invalid."""
+    bits = _load(cfg).get("weight_bits", {})
+    if not isinstance(bits, dict):
+        raise ValueError("'weight_bits' must map layer names to 4 or 6")
+    names = [l[0] for l in layers]
+    unknown = sorted(set(bits) - set(names))
+    if unknown:
+        raise ValueError(f"weight_bits: unknown layers {unknown}")
+    for n in bits:
+        if bits[n] not in (4, 6):
+            raise ValueError(f"weight_bits[{n!r}] = {bits[n]!r}, not 4 or 6")
+    return {n: int(bits.get(n, 6)) for n in names}
+
+
+def parse_config(cfg, layers):
+    """(group size, {layer name: activation bits}) from a config dict or the
+    path of a JSON file; raises ValueError on anything missing or invalid."""
+    cfg = _load(cfg)
     gs = cfg.get("group_size", 128)
     if gs not in (32, 64, 128, 256):
         raise ValueError(f"group_size {gs!r} not in (32, 64, 128, 256)")
@@ -70,11 +99,16 @@ def parse_config(cfg, layers):
     missing = [n for n in names if n not in bits]
     if unknown or missing:
         raise ValueError(f"act_bits: unknown layers {unknown}, missing layers {missing}")
+    weight_bits = parse_weight_bits(cfg, layers)
     for n in names:
-        if bits[n] not in (6, 8):
+        if weight_bits[n] == 4:
+            if bits[n] != 16:
+                raise ValueError(f"act_bits[{n!r}] = {bits[n]!r}: layers with 4-bit weights take 16")
+        elif bits[n] not in (6, 8):
             raise ValueError(f"act_bits[{n!r}] = {bits[n]!r}, not 6 or 8")
     for name, N, K, _ in layers:
-        if flexq.weight_packed_bytes(N, K, gs) == 0:
+        size = flexq.weight4_packed_bytes if weight_bits[name] == 4 else flexq.weight_packed_bytes
+        if size(N, K, gs) == 0:
             raise ValueError(f"layer {name}: {N}x{K} not supported with group size {gs}")
     return gs, {n: int(bits[n]) for n in names}
 
@@ -127,7 +161,8 @@ class LayerStack:
                 w = weight(members[0][0], members[0][1], K)
             else:
                 w = torch.cat([weight(name, N, K) for name, N, _ in members], dim=0)
-            self.packed[key] = flexq.quantize_weight(w, self.gs)
+            pack = flexq.quantize_weight4 if bits == 16 else flexq.quantize_weight
+            self.packed[key] = pack(w, self.gs)
             del w
         # grouped calls: the units of one (site, bits), in order of first use
         self.groups = []
@@ -163,12 +198,15 @@ class LayerStack:
             n = 0
             for g in self.groups:
                 K = self.units[g[0]][3]
+                if self.units[g[0]][2] == 16:
+                    n += 1
+                    continue
                 n += flexq.group_plan(M, K, self.gs, [self.units[i][5] for i in g])[3]
             return n
         n, quantized = 0, set()
         for key, site, bits, K, members, n_total in self.units:
             q = (site, bits)
-            if q in quantized or flexq.linear_launches(M, n_total, K, self.gs) == 1:
+            if bits == 16 or q in quantized or flexq.linear_launches(M, n_total, K, self.gs) == 1:
                 n += 1
             else:
                 n += 2
@@ -195,7 +233,10 @@ class LayerStack:
                 key, site, bits, K, members, n_total = self.units[g[0]]
                 weights = [self.packed[self.units[i][0]] + (self.units[i][5],) for i in g]
                 outs = [out.get(self.units[i][4][0][0]) for i in g]
-                ys = flexq.linear_group(acts[site], weights, self.gs, bits, outs=outs)
+                if bits == 16:
+                    ys = flexq.linear4_group(acts[site], weights, self.gs, outs=outs)
+                else:
+                    ys = flexq.linear_group(acts[site], weights, self.gs, bits, outs=outs)
                 for i, y in zip(g, ys):
                     out[self.units[i][4][0][0]] = y
             return out
@@ -210,7 +251,9 @@ class LayerStack:
                     y = torch.empty(M, n_total, dtype=torch.float16, device=self.device)
                     self._ybuf[(key, M)] = y
             q = (site, bits)
-            if q not in codes and flexq.linear_launches(M, n_total, K, self.gs) == 1:
+            if bits == 16:
+                y = flexq.linear4(acts[site], wp, ws, n_total, self.gs, out=y)
+            elif q not in codes and flexq.linear_launches(M, n_total, K, self.gs) == 1:
                 y = flexq.linear(acts[site], wp, ws, n_total, self.gs, bits, out=y)
             else:
                 if q not in codes:

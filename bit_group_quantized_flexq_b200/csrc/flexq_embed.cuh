@@ -170,11 +170,12 @@ struct SortArgs {
 };
 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs a) {
-  __shared__ unsigned hist[kSortWarps][kSortDigits];
+  __shared__ unsigned hist[kSortWarps][kSortDigits + 1];   // the odd stride spreads a digit's column
   __shared__ unsigned total[kSortDigits];
   __shared__ unsigned base[kSortDigits];
   __shared__ unsigned warp_sum[kSortDigits / 32];
   const int C = a.clusters_size;
+  grid_launch_dependents();         // the sums wait for this kernel's end
   if (static_cast<int>(blockIdx.x) >= C) {
     const long long stride = static_cast<long long>(gridDim.x - C) * kSortThreads;
 #pragma unroll
@@ -190,7 +191,9 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned below = (1u << lane) - 1u;
   const int rank = blockIdx.x;
-  // each warp owns a run of consecutive tokens
+  // each warp owns a run of consecutive tokens; the first kKeep of a lane stay
+  // in registers between counting and placing them
+  constexpr int kKeep = 4;
   const long long per_warp = ((static_cast<long long>(a.T) + kSortWarps * C - 1) / (kSortWarps * C) + 31) / 32 * 32;
   const long long lo = min(static_cast<long long>(a.T), (static_cast<long long>(rank) * kSortWarps + warp) * per_warp);
   const long long hi = min(static_cast<long long>(a.T), lo + per_warp);
@@ -200,43 +203,86 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     const uint2* src = a.buf[(pass + 1) & 1];
     uint2* dst = a.buf[pass & 1];
     auto item = [&](long long i) {
+      if (i >= hi) return make_uint2(0, 0);
       if (pass == 0) {
         const int v = token_row(a.ids, a.id_bytes, i, a.V);
         return make_uint2(v < 0 ? a.V : v, static_cast<unsigned>(i));
       }
       return __ldcg(src + i);
     };
-    for (int i = lane; i < kSortDigits; i += 32) hist[warp][i] = 0;
-    __syncwarp();
-    for (long long i0 = lo; i0 < hi; i0 += 32) {
-      const bool in = i0 + lane < hi;
-      const unsigned d = in ? (item(i0 + lane).x >> shift) & 255u : 256u;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+    // the lanes whose token has this lane's digit
+    auto alike = [&](unsigned d, bool in) {
+      unsigned same = __ballot_sync(0xFFFFFFFFu, in);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const unsigned set = __ballot_sync(0xFFFFFFFFu, d >> b & 1u);
+        same &= d >> b & 1u ? set : ~set;
+      }
+      return same;
+    };
+    auto count = [&](const uint2& it, bool in) {
+      const unsigned d = (it.x >> shift) & 255u, same = alike(d, in);
       if (in && (same & below) == 0) hist[warp][d] += __popc(same);
       __syncwarp();
-    }
-    __syncthreads();
-    if (threadIdx.x < kSortDigits) {           // each warp's first place within the CTA
-      unsigned sum = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const unsigned c = hist[w][threadIdx.x];
-        hist[w][threadIdx.x] = sum;
-        sum += c;
+    };
+    auto place = [&](const uint2& it, bool in) {
+      const unsigned d = (it.x >> shift) & 255u, same = alike(d, in);
+      const unsigned at = hist[warp][d];
+      __syncwarp();
+      if (in) {
+        dst[base[d] + at + __popc(same & below)] = it;
+        if ((same & below) == 0) hist[warp][d] = at + __popc(same);
       }
-      total[threadIdx.x] = sum;
+      __syncwarp();
+    };
+    uint2 kept[kKeep];
+#pragma unroll
+    for (int r = 0; r < kKeep; ++r) kept[r] = item(lo + 32 * r + lane);
+    for (int i = lane; i < kSortDigits; i += 32) hist[warp][i] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kKeep; ++r)
+      if (lo + 32 * r < hi) count(kept[r], lo + 32 * r + lane < hi);
+    for (long long i0 = lo + 32 * kKeep; i0 < hi; i0 += 32) count(item(i0 + lane), i0 + lane < hi);
+    __syncthreads();
+    {                               // each warp's first place within the CTA, four threads to a digit
+      const int d = threadIdx.x >> 2, q = threadIdx.x & 3;
+      unsigned c[8], sum = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        c[w] = hist[8 * q + w][d];
+        sum += c[w];
+      }
+      unsigned incl = sum;
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const unsigned up = __shfl_up_sync(0xFFFFFFFFu, incl, o, 4);
+        if (q >= o) incl += up;
+      }
+      unsigned at = incl - sum;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        hist[8 * q + w][d] = at;
+        at += c[w];
+      }
+      if (q == 3) total[d] = incl;
     }
     if (C > 1) cluster_sync_all(); else __syncthreads();
     unsigned all = 0, before = 0, incl = 0;
     if (threadIdx.x < kSortDigits) {
-      for (int r = 0; r < C; ++r) {
-        unsigned c;
-        if (C > 1)
+      if (C > 1) {
+        unsigned c[8];              // all at once; C is 8
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
           asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                       : "=r"(c) : "r"(map_to_rank(smem_u32(&total[threadIdx.x]), r)) : "memory");
-        else
-          c = total[threadIdx.x];
-        all += c;
-        if (r < rank) before += c;
+                       : "=r"(c[r]) : "r"(map_to_rank(smem_u32(&total[threadIdx.x]), r)) : "memory");
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          all += c[r];
+          if (r < rank) before += c[r];
+        }
+      } else {
+        all = total[threadIdx.x];
       }
       incl = all;
 #pragma unroll
@@ -249,23 +295,16 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     __syncthreads();
     if (threadIdx.x < kSortDigits) {
       unsigned low = 0;
-      for (int w = 0; w < warp; ++w) low += warp_sum[w];
+#pragma unroll
+      for (int w = 0; w < kSortDigits / 32; ++w)
+        if (w < warp) low += warp_sum[w];
       base[threadIdx.x] = low + incl - all + before;
     }
     __syncthreads();
-    for (long long i0 = lo; i0 < hi; i0 += 32) {
-      const bool in = i0 + lane < hi;
-      const uint2 it = in ? item(i0 + lane) : make_uint2(0, 0);
-      const unsigned d = in ? (it.x >> shift) & 255u : 256u;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
-      const unsigned at = in ? hist[warp][d] : 0;
-      __syncwarp();
-      if (in) {
-        dst[base[d] + at + __popc(same & below)] = it;
-        if ((same & below) == 0) hist[warp][d] = at + __popc(same);
-      }
-      __syncwarp();
-    }
+#pragma unroll
+    for (int r = 0; r < kKeep; ++r)
+      if (lo + 32 * r < hi) place(kept[r], lo + 32 * r + lane < hi);
+    for (long long i0 = lo + 32 * kKeep; i0 < hi; i0 += 32) place(item(i0 + lane), i0 + lane < hi);
     // the next pass reads what every CTA of the cluster wrote, and none
     // clears its counts while another reads them
     if (C > 1) cluster_sync_all(); else __syncthreads();
@@ -383,6 +422,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, 
   __shared__ int valid;
   const int tid = threadIdx.x;
   const long long p0 = static_cast<long long>(blockIdx.x) * a.tile;
+  grid_launch_dependents();
+  grid_wait_dependencies();
   if (tid == 0) valid = 0;
   __syncthreads();
   if (tid < a.tile && p0 + tid < a.T) {
@@ -464,6 +505,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, 
 template <typename T, typename TO, int BITS>
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const Table tb, const SumArgs a) {
   const long long end = (static_cast<long long>(blockIdx.x) + 1) * a.tile;   // of the tile
+  grid_wait_dependencies();
   if (end >= a.T) return;
   const unsigned v = a.sorted[end - 1].x;
   if (v >= static_cast<unsigned>(tb.V) || a.sorted[end].x != v) return;
@@ -511,11 +553,11 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const Table tb,
 }
 
 // ------------------------------------------------------------- few tokens ----
-// Up to 128 tokens take one launch: every CTA sorts them all by comparing each
+// Up to 256 tokens take one launch: every CTA sorts them all by comparing each
 // with each (a microsecond, hidden behind nothing but cheaper than the three
 // launches above), then takes its share of the runs' 2048-column pieces, and of
 // the rows without a token, whose gradients it zeroes.
-constexpr int kFewTokens = 128;
+constexpr int kFewTokens = 256;
 
 struct FewArgs {
   SumArgs sum;
@@ -539,6 +581,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_few_kernel(const Table tb, 
   if (tid < n) {
     const int v = row_of[tid];
     int at = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) at += row_of[j] < v || (row_of[j] == v && j < tid);
     items[at] = make_uint2(static_cast<unsigned>(v), static_cast<unsigned>(tid));
   }
@@ -606,10 +649,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_few_kernel(const Table tb, 
   };
   const int share_lo = static_cast<int>(static_cast<long long>(blockIdx.x) * tb.V / gridDim.x);
   const int share_hi = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * tb.V / gridDim.x);
-  int lo = share_lo;
-  for (int r = 0; r <= runs && lo < share_hi; ++r) {
+  int lo = share_lo, r0 = 0, r1 = runs;               // the first run from here on
+  while (r0 < r1) {
+    const int mid = (r0 + r1) / 2;
+    if (static_cast<int>(items[start[mid]].x) < share_lo) r0 = mid + 1; else r1 = mid;
+  }
+  for (int r = r0; r <= runs && lo < share_hi; ++r) {
     const int row = r < runs ? static_cast<int>(items[start[r]].x) : tb.V;
-    if (row < lo) continue;
     const int hi = min(row, share_hi);
     if (lo < hi) zero_rows(lo, hi);
     lo = row + 1;

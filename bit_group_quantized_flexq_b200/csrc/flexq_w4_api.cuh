@@ -400,9 +400,22 @@ cudaError_t launch_sums(const flexq::Table& tb, const flexq::SumArgs& a, cudaStr
   if (e != cudaSuccess) return e;
   const unsigned tiles = static_cast<unsigned>((a.T + static_cast<long long>(a.tile) - 1) / a.tile);
   const unsigned pieces = static_cast<unsigned>((tb.K + flexq::kSumCols - 1) / flexq::kSumCols);
-  flexq::embed_sum_kernel<T, TO, BITS><<<dim3(tiles, (pieces + 1) / 2), flexq::kSumThreads, smem, s>>>(tb, a);
-  if (tiles > 1) flexq::embed_join_kernel<T, TO, BITS><<<dim3(tiles, pieces), flexq::kSumThreads, 0, s>>>(tb, a);
-  return cudaGetLastError();
+  // each launch's set-up overlaps the end of the one before
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, (pieces + 1) / 2);
+  cfg.blockDim = dim3(flexq::kSumThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t sum = cudaLaunchKernelEx(&cfg, flexq::embed_sum_kernel<T, TO, BITS>, tb, a);
+  if (sum != cudaSuccess || tiles == 1) return sum;
+  cfg.gridDim = dim3(tiles, pieces);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, flexq::embed_join_kernel<T, TO, BITS>, tb, a);
 }
 
 template <typename T, typename TO>

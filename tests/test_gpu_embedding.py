@@ -117,6 +117,10 @@ def check_backward(table_grad, scales_grad, dy, ids, q, gs, bits, scale, table_d
     (3, 4160, 64, 4, 129, "any", torch.bfloat16, torch.bfloat16),
     (3, 4160, 64, 4, 128, "any", torch.float16, torch.float32),
     (2000, 160, 32, 4, 100, "heavy", torch.bfloat16, torch.bfloat16),
+    (500, 96, 32, 4, 256, "heavy", torch.bfloat16, torch.float32),
+    (500, 96, 32, 4, 257, "heavy", torch.float16, torch.float16),
+    (128, 512, 64, 6, 700, "same", torch.float16, torch.float16),
+    (300, 64, 64, 4, 40000, "heavy", torch.float16, torch.float32),
     (128, 512, 64, 6, 128, "distinct", torch.float16, torch.float16),
     (384, 256, 256, 6, 77, "padding", torch.bfloat16, torch.float32),
     (1000, 256, 256, 4, 1024, "distinct", torch.float16, torch.float16),
@@ -245,8 +249,8 @@ def test_refusals_on_the_gpu():
     with pytest.raises(ValueError, match="nothing to compute"):
         flexq.embedding_backward(dy, ids, wp, V, gs, with_scales=False)
     with pytest.raises(flexq.FlexQError, match="workspace"):
-        many = torch.zeros(200, dtype=torch.int64, device="cuda")
-        flexq.embedding_backward(torch.zeros(200, K, dtype=torch.float16, device="cuda"), many, wp, V, gs,
+        many = torch.zeros(300, dtype=torch.int64, device="cuda")
+        flexq.embedding_backward(torch.zeros(300, K, dtype=torch.float16, device="cuda"), many, wp, V, gs,
                                  workspace_buf=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="contiguous"):
         flexq.embedding_backward(dy[:, ::2][:, :128].expand(3, 128), ids, wp, V, gs)

@@ -206,7 +206,7 @@ int encode_w4_map(CUtensorMap* map, const void* wp, int N, int kbs, int strips) 
 // every group of SMs), each with at least four column tiles.
 int w4_mma_split(long long tiles, int kbs, long long slots) {
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= slots * 15 / 16 && kbs >= 8 * split) split *= 2;
+  while (split < 8 && tiles * (split + 1) <= slots * 15 / 16 && kbs >= 4 * (split + 1)) ++split;
   return split;
 }
 
@@ -269,11 +269,23 @@ int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, i
   m.gs_shift = a.gs_shift;
   m.status = a.status;
   m.wait_limit_ns = a.wait_limit_ns;
-  return a.M <= 16    ? launch_w4_mma<E, 16, 1>(m, L, a.x, a.ldx, sms, s)
-         : a.M <= 32  ? launch_w4_mma<E, 32, 1>(m, L, a.x, a.ldx, sms, s)
-         : a.M <= 64  ? launch_w4_mma<E, 64, 1>(m, L, a.x, a.ldx, sms, s)
-         : a.M <= 256 ? launch_w4_mma<E, 128, 1>(m, L, a.x, a.ldx, sms, s)
-                      : launch_w4_mma<E, 128, 2>(m, L, a.x, a.ldx, sms, s);
+  // Two row blocks per CTA bring the activations half as often, once there are
+  // tiles enough for a good part of the SMs: 28672 x 8192 at 64 tokens 53 us
+  // with two and 68 with one, 11008 x 4096 at 256 tokens 30 and 34, but 1000 x
+  // 2048 at 128 tokens 14.5 and 10.4.
+  const int T = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  long long tiles = 0;
+  for (int l = 0; l < L.n; ++l) tiles += (L.N[l] + 255) / 256;
+  const bool two = T >= 32 && tiles * ((a.M + T - 1) / T) * 5 >= sms;
+  switch (T) {
+    case 16: return launch_w4_mma<E, 16, 1>(m, L, a.x, a.ldx, sms, s);
+    case 32: return two ? launch_w4_mma<E, 32, 2>(m, L, a.x, a.ldx, sms, s)
+                        : launch_w4_mma<E, 32, 1>(m, L, a.x, a.ldx, sms, s);
+    case 64: return two ? launch_w4_mma<E, 64, 2>(m, L, a.x, a.ldx, sms, s)
+                        : launch_w4_mma<E, 64, 1>(m, L, a.x, a.ldx, sms, s);
+    default: return two ? launch_w4_mma<E, 128, 2>(m, L, a.x, a.ldx, sms, s)
+                        : launch_w4_mma<E, 128, 1>(m, L, a.x, a.ldx, sms, s);
+  }
 }
 
 int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long ldx, int n_layers,

@@ -133,9 +133,9 @@ struct W4MmaCfg {
   static constexpr int kRows = 128 * RB;
   static constexpr int kXBox = T * 128;                 // 64 columns of T tokens
   static constexpr int kXSlot = 2 * kXBox;
-  static constexpr int kXSlots = RB == 2 ? 4 : T == 128 ? 2 : T == 64 ? 4 : T == 32 ? 6 : 8;
+  static constexpr int kXSlots = RB == 2 ? (T == 128 ? 4 : 6) : T == 128 ? 2 : T == 64 ? 4 : T == 32 ? 6 : 8;
   static constexpr int kWSlot = 8 * RB * kW4TileBytes;  // 128 columns of the rows
-  static constexpr int kWSlots = T == 128 ? 4 : T == 16 ? 6 : 5;
+  static constexpr int kWSlots = T == 128 ? 4 : RB == 2 ? 6 : T == 16 ? 6 : 5;
   static constexpr int kXBytes = kXSlots * kXSlot;
   static constexpr int kWBytes = kWSlots * kWSlot;
   // results lie over the operand slots before they leave, or FP32 sums for

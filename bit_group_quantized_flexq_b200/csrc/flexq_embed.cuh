@@ -152,7 +152,9 @@ __global__ void __launch_bounds__(kLookThreads) embed_kernel(const Table tb, con
 // least-significant-digit radix sort of 8-bit digits.  One cluster sorts;
 // its CTAs exchange digit counts in distributed shared memory and meet at
 // the cluster's barrier, so that one launch does every pass.  The grid's
-// other clusters meanwhile zero the outputs.
+// other clusters meanwhile zero the scales' gradient and what of the rows'
+// they can in that time; the rest of it, but for the rows with a token, is
+// zeroed beside the sums.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortDigits = 256;
@@ -166,6 +168,7 @@ struct SortArgs {
   long long fill_n[2];
   float* tail;                    // the last 0..3 floats of the second output
   int tail_n;
+  unsigned* present;              // a bit per row that has a token, or null
   int clusters_size;              // CTAs of the sorting cluster
 };
 
@@ -198,6 +201,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
   const long long lo = min(static_cast<long long>(a.T), (static_cast<long long>(rank) * kSortWarps + warp) * per_warp);
   const long long hi = min(static_cast<long long>(a.T), lo + per_warp);
 
+  if (a.present)                    // in place before the first tokens are placed
+    for (int i = rank * kSortThreads + threadIdx.x; i < (a.V + 31) / 32; i += C * kSortThreads) a.present[i] = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = 8 * pass;
     const uint2* src = a.buf[(pass + 1) & 1];
@@ -231,6 +236,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
       __syncwarp();
       if (in) {
         dst[base[d] + at + __popc(same & below)] = it;
+        if (pass == 0 && a.present && it.x < static_cast<unsigned>(a.V)) atomicOr(&a.present[it.x >> 5], 1u << (it.x & 31));
         if ((same & below) == 0) hist[warp][d] = at + __popc(same);
       }
       __syncwarp();
@@ -324,6 +330,8 @@ struct SumArgs {
   float* partial;                 // [tiles][2][K]: a tile's part of a run it shares with others
   void* table;                    // row gradient, or null
   float* scales;                  // scale gradient, or null
+  const unsigned* present;        // rows of the table with a token
+  int fill_row, sum_ctas, fill_ctas;    // rows from fill_row on are zeroed beside the sums
 };
 
 // Writes the finished sums of columns k .. k+7 of row v; codes: the row's, where
@@ -421,9 +429,27 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, 
   __shared__ Item items[kSumMaxTile];
   __shared__ int valid;
   const int tid = threadIdx.x;
-  const long long p0 = static_cast<long long>(blockIdx.x) * a.tile;
   grid_launch_dependents();
   grid_wait_dependencies();
+  // sums and zeros take turns, so that dY is read while zeros are written
+  const int pairs = min(a.sum_ctas, a.fill_ctas), block = blockIdx.x;
+  const bool fills = block < 2 * pairs ? block & 1 : a.fill_ctas > a.sum_ctas;
+  const int id = block < 2 * pairs ? block >> 1 : block - pairs;
+  if (fills) {
+    const int rows = tb.V - a.fill_row;
+    const int lo = a.fill_row + static_cast<int>(static_cast<long long>(id) * rows / a.fill_ctas);
+    const int hi = a.fill_row + static_cast<int>(static_cast<long long>(id + 1) * rows / a.fill_ctas);
+    const int pieces = tb.K * static_cast<int>(sizeof(TO)) / 16;
+    for (int v = lo; v < hi; ++v) {
+      if (a.present[v >> 5] >> (v & 31) & 1u) continue;
+      uint4* row = reinterpret_cast<uint4*>(static_cast<TO*>(a.table) + static_cast<size_t>(v) * tb.K);
+      for (int i = tid; i < pieces; i += kSumThreads) row[i] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int tiles = static_cast<int>((static_cast<long long>(a.T) + a.tile - 1) / a.tile);
+  const int tile = id % tiles, column = id / tiles;
+  const long long p0 = static_cast<long long>(tile) * a.tile;
   if (tid == 0) valid = 0;
   __syncthreads();
   if (tid < a.tile && p0 + tid < a.T) {
@@ -443,7 +469,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, 
   }
   __syncthreads();
   const int n = valid;
-  const int k0 = blockIdx.y * (2 * kSumCols) + tid * 8;
+  const int k0 = column * (2 * kSumCols) + tid * 8;
   uint32_t at[2][Codes8<BITS>::kWords];
   Codes8<BITS>::places(k0, at[0]);
   Codes8<BITS>::places(k0 + kSumCols, at[1]);
@@ -487,7 +513,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const Table tb, 
           embed_finish<T, TO, BITS>(tb, a, items[i].row, k, k < tb.K, acc[u], codes);
         } else if (k < tb.K) {
           float4* p = reinterpret_cast<float4*>(
-              a.partial + (static_cast<size_t>(blockIdx.x) * 2 + (next == kOpen ? 1 : 0)) * tb.K + k);
+              a.partial + (static_cast<size_t>(tile) * 2 + (next == kOpen ? 1 : 0)) * tb.K + k);
           p[0] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
           p[1] = make_float4(acc[u][4], acc[u][5], acc[u][6], acc[u][7]);
         }

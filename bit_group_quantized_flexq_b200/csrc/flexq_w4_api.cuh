@@ -391,12 +391,18 @@ int sum_tile(long long T, int K) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-size_t backward_workspace(long long T, int K) {
+size_t present_bytes(int V) { return align256((static_cast<size_t>(V) + 31) / 32 * sizeof(unsigned)); }
+
+size_t backward_workspace(long long T, int V, int K) {
   if (T <= flexq::kFewTokens) return 0;
   const long long tiles = (T + sum_tile(T, K) - 1) / sum_tile(T, K);
-  return 2 * align256(static_cast<size_t>(T) * sizeof(uint2)) +
+  return 2 * align256(static_cast<size_t>(T) * sizeof(uint2)) + present_bytes(V) +
          static_cast<size_t>(tiles) * 2 * K * sizeof(float);
 }
+
+// Bytes of the rows' gradient that are zeroed while the tokens are sorted;
+// more would outlast the sort.
+constexpr size_t kSortFill = 64u << 20;
 
 template <typename T, typename TO>
 void launch_few(int bits, const flexq::Table& tb, const flexq::FewArgs& f, unsigned grid, cudaStream_t s) {
@@ -405,7 +411,7 @@ void launch_few(int bits, const flexq::Table& tb, const flexq::FewArgs& f, unsig
 }
 
 template <typename T, typename TO, int BITS>
-cudaError_t launch_sums(const flexq::Table& tb, const flexq::SumArgs& a, cudaStream_t s) {
+cudaError_t launch_sums(const flexq::Table& tb, flexq::SumArgs a, cudaStream_t s) {
   static std::atomic<unsigned long long> ready{0};
   constexpr int smem = static_cast<int>(sizeof(flexq::SumRing<BITS>));
   const cudaError_t e = allow_smem(flexq::embed_sum_kernel<T, TO, BITS>, smem, ready);
@@ -414,7 +420,8 @@ cudaError_t launch_sums(const flexq::Table& tb, const flexq::SumArgs& a, cudaStr
   const unsigned pieces = static_cast<unsigned>((tb.K + flexq::kSumCols - 1) / flexq::kSumCols);
   // each launch's set-up overlaps the end of the one before
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles, (pieces + 1) / 2);
+  a.sum_ctas = static_cast<int>(tiles * ((pieces + 1) / 2));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.sum_ctas + a.fill_ctas));
   cfg.blockDim = dim3(flexq::kSumThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -512,9 +519,9 @@ int flexq_embedding(long long T, int V, int K, int group_size, int weight_bits, 
   return ok();
 }
 
-size_t flexq_embedding_backward_workspace_bytes(long long T, int K) {
-  if (T <= 0 || T > INT32_MAX || K <= 0 || K > (1 << 24)) return 0;
-  return backward_workspace(T, K);
+size_t flexq_embedding_backward_workspace_bytes(long long T, int V, int K) {
+  if (T <= 0 || T > INT32_MAX || V <= 0 || V > (1 << 30) || K <= 0 || K > (1 << 24)) return 0;
+  return backward_workspace(T, V, K);
 }
 
 int flexq_embedding_backward(long long T, int V, int K, int group_size, int weight_bits, int dtype,
@@ -528,7 +535,7 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
     return fail(FLEXQ_ERR_INVALID_ARG, "table_dtype=%d is neither dY's type nor FLEXQ_DTYPE_FP32", table_dtype);
   if (!aligned16(d_table) || !aligned16(d_scales))
     return fail(FLEXQ_ERR_MISALIGNED, "d_table or d_scales is not 16-byte aligned");
-  const size_t need = backward_workspace(T, K);
+  const size_t need = backward_workspace(T, V, K);
   if (T > 0) {
     const void* ptrs[] = {dY, workspace};
     const char* names[] = {"dY", "workspace"};
@@ -582,9 +589,20 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
   const size_t table_bytes =
       d_table ? static_cast<size_t>(V) * K * (table_dtype == FLEXQ_DTYPE_FP32 ? 4 : 2) : 0;
   const size_t scale_elems = d_scales ? static_cast<size_t>(V) * (K / group_size) : 0;
+  const size_t row_bytes = table_bytes / static_cast<size_t>(V);
+  if (d_table) {
+    a.fill_row = static_cast<int>(std::min<size_t>(static_cast<size_t>(V), kSortFill / row_bytes));
+    // the rest in pieces of about 256 KB
+    if (a.fill_row < V) {
+      const size_t rest = table_bytes - static_cast<size_t>(a.fill_row) * row_bytes;
+      a.fill_ctas = static_cast<int>(std::min<size_t>(std::max<size_t>(1, rest >> 18), static_cast<size_t>(V - a.fill_row)));
+      so.present = reinterpret_cast<unsigned*>(ws + 2 * item_bytes);
+      a.present = so.present;
+    }
+  }
   so.fill[0] = static_cast<uint4*>(d_table);
   so.fill[1] = reinterpret_cast<uint4*>(d_scales);
-  so.fill_n[0] = static_cast<long long>(table_bytes / 16);
+  so.fill_n[0] = static_cast<long long>(static_cast<size_t>(a.fill_row) * row_bytes / 16);
   so.fill_n[1] = static_cast<long long>(scale_elems / 4);
   so.tail = d_scales + scale_elems / 4 * 4;
   so.tail_n = static_cast<int>(scale_elems % 4);
@@ -608,7 +626,7 @@ int flexq_embedding_backward(long long T, int V, int K, int group_size, int weig
 
   a.sorted = so.buf[(so.passes - 1) & 1];
   a.tile = sum_tile(T, K);
-  a.partial = reinterpret_cast<float*>(ws + 2 * item_bytes);
+  a.partial = reinterpret_cast<float*>(ws + 2 * item_bytes + present_bytes(V));
   if (dtype == FLEXQ_DTYPE_FP16)
     e = wide ? launch_sums_bits<__half, float>(weight_bits, tb, a, cfg.stream)
              : launch_sums_bits<__half, __half>(weight_bits, tb, a, cfg.stream);

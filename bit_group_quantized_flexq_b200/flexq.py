@@ -126,7 +126,7 @@ def lib():
                                               c_void_p, c_void_p]),
             "flexq_embedding": (c_int, [c_ll, c_int, c_int, c_int, c_int, c_int, c_void_p, c_int,
                                         c_void_p, c_void_p, ctypes.c_float, c_void_p, c_void_p]),
-            "flexq_embedding_backward_workspace_bytes": (c_size_t, [c_ll, c_int]),
+            "flexq_embedding_backward_workspace_bytes": (c_size_t, [c_ll, c_int, c_int]),
             "flexq_embedding_backward": (c_int, [c_ll, c_int, c_int, c_int, c_int, c_int, c_void_p,
                                                  c_int, c_void_p, c_void_p, ctypes.c_float, c_int,
                                                  c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
@@ -662,13 +662,14 @@ def linear4_group(x, weights, group_size, outs=None):
 
 
 def _check_ids(ids):
-    if not isinstance(ids, torch.Tensor):
+    if not isinstance(ids, _Tensor):
         raise TypeError("ids must be a torch.Tensor")
-    if ids.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    dtype = ids.dtype
+    if dtype is not torch.int64 and dtype is not torch.int32:
+        raise ValueError(f"ids must be torch.int32 or torch.int64, got {dtype}")
     if not (ids.is_cuda and ids.is_contiguous()):
-        _need(ids, "ids", ids.dtype)
-    return ids.get_device(), 8 if ids.dtype is torch.int64 else 4
+        _need(ids, "ids", dtype)
+    return ids.get_device(), 8 if dtype is torch.int64 else 4
 
 
 def _table_bytes(V, K, group_size, weight_bits):
@@ -676,11 +677,10 @@ def _table_bytes(V, K, group_size, weight_bits):
         return _w4_bytes(V, K, group_size, "table")
     if weight_bits != 6:
         raise ValueError(f"weight_bits must be 4 or 6, got {weight_bits!r}")
-    nbytes = weight_packed_bytes(V, K, group_size)
-    if nbytes == 0:
+    if V <= 0 or K <= 0 or V % 128 or K % 256 or group_size not in (32, 64, 128, 256):
         raise FlexQError(FLEXQ_ERR_UNSUPPORTED,
                          f"unsupported table shape {V}x{K}, gs={group_size}, 6 bits")
-    return nbytes
+    return V * K // 4 * 3
 
 
 def _scales_shape(V, K, group_size, weight_bits):
@@ -694,18 +694,19 @@ def embedding(ids, wp, ws, V, group_size, scale=1.0, weight_bits=4, dtype=torch.
     quantize_weight4 (weight_bits 4) or quantize_weight (6, byte-aligned
     layout).  A token outside [0, V) is padding: its row is zero."""
     dev, id_bytes = _check_ids(ids)
-    if dtype not in (torch.float16, torch.bfloat16):
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
-    if not isinstance(ws, torch.Tensor) or ws.dim() != 2:
+    if not isinstance(ws, _Tensor) or ws.dim() != 2:
         raise ValueError("ws must be a tensor with two dimensions")
-    K = ws.shape[0 if weight_bits == 6 else 1] * group_size
+    rows, cols = ws.shape
+    K, scales = (rows * group_size, (rows, V)) if weight_bits == 6 else (cols * group_size, (V, cols))
     nbytes, shape = _table_bytes(V, K, group_size, weight_bits), (*ids.shape, K)
     if not _is(wp, torch.uint8, (nbytes,), dev):
         _refuse(wp, "wp", torch.uint8, (nbytes,), ids)
-    if not _is(ws, torch.float16, _scales_shape(V, K, group_size, weight_bits), dev):
-        _refuse(ws, "ws", torch.float16, _scales_shape(V, K, group_size, weight_bits), ids)
+    if not _is(ws, torch.float16, scales, dev):
+        _refuse(ws, "ws", torch.float16, scales, ids)
     if out is None:
-        out = ws.new_empty(shape, dtype=dtype)
+        out = ws.new_empty(shape) if dtype is torch.float16 else ws.new_empty(shape, dtype=dtype)
     elif not _is(out, dtype, shape, dev):
         _refuse(out, "out", dtype, shape, ids)
     _launch(dev, lib().flexq_embedding, ids.numel(), V, K, group_size, weight_bits, _DTYPES[dtype],
@@ -713,8 +714,8 @@ def embedding(ids, wp, ws, V, group_size, scale=1.0, weight_bits=4, dtype=torch.
     return out
 
 
-def embedding_backward_workspace_bytes(T, K):
-    return int(lib().flexq_embedding_backward_workspace_bytes(T, K))
+def embedding_backward_workspace_bytes(T, V, K):
+    return int(lib().flexq_embedding_backward_workspace_bytes(T, V, K))
 
 
 def embedding_backward(dy, ids, wp, V, group_size, scale=1.0, weight_bits=4, table_dtype=None,
@@ -728,7 +729,7 @@ def embedding_backward(dy, ids, wp, V, group_size, scale=1.0, weight_bits=4, tab
 
     out:           (rows, scales) to write into;
     workspace_buf: a uint8 device tensor of at least
-                   embedding_backward_workspace_bytes(tokens, K) bytes that no
+                   embedding_backward_workspace_bytes(tokens, V, K) bytes that no
                    other running call uses; by default one of this call's own."""
     dtype, dev = _activation(dy, "dy")
     ids_dev, id_bytes = _check_ids(ids)
@@ -759,7 +760,7 @@ def embedding_backward(dy, ids, wp, V, group_size, scale=1.0, weight_bits=4, tab
     elif not _is(scales, torch.float32, shape, dev):
         _refuse(scales, "scales", torch.float32, shape, dy)
     if workspace_buf is None:
-        workspace_buf = torch.empty(embedding_backward_workspace_bytes(T, K), dtype=torch.uint8,
+        workspace_buf = torch.empty(embedding_backward_workspace_bytes(T, V, K), dtype=torch.uint8,
                                     device=dy.device)
     elif not _is(workspace_buf, torch.uint8, (workspace_buf.numel(),), dev):
         _refuse(workspace_buf, "workspace", torch.uint8, (workspace_buf.numel(),), dy)

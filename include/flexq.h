@@ -450,7 +450,7 @@ int flexq_embedding(long long T, int V, int K, int group_size, int weight_bits, 
 
 /* Device scratch of flexq_embedding_backward (need not be cleared; 0 for few
  * tokens, where workspace may be NULL). */
-size_t flexq_embedding_backward_workspace_bytes(long long T, int K);
+size_t flexq_embedding_backward_workspace_bytes(long long T, int V, int K);
 
 /*
  * flexq_embedding_backward -- the gradient of flexq_embedding from dY [T, K]
@@ -466,7 +466,7 @@ size_t flexq_embedding_backward_workspace_bytes(long long T, int K);
  * zeros.  Tokens are sorted by row and each row's are added in FP32 in the
  * order of the tokens, in pieces whose bounds depend on T and K alone: the
  * result does not vary from run to run.
- *   workspace  flexq_embedding_backward_workspace_bytes(T, K) bytes, 16-byte
+ *   workspace  flexq_embedding_backward_workspace_bytes(T, V, K) bytes, 16-byte
  *              aligned, used by this call only while it runs.
  */
 int flexq_embedding_backward(long long T, int V, int K, int group_size, int weight_bits, int dtype,

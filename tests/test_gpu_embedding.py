@@ -121,6 +121,8 @@ def check_backward(table_grad, scales_grad, dy, ids, q, gs, bits, scale, table_d
     (500, 96, 32, 4, 257, "heavy", torch.float16, torch.float16),
     (128, 512, 64, 6, 700, "same", torch.float16, torch.float16),
     (300, 64, 64, 4, 40000, "heavy", torch.float16, torch.float32),
+    (20001, 1024, 128, 4, 700, "heavy", torch.float16, torch.float32),    # 82 MB of rows
+    (9088, 4096, 256, 6, 3000, "any", torch.bfloat16, torch.bfloat16),
     (128, 512, 64, 6, 128, "distinct", torch.float16, torch.float16),
     (384, 256, 256, 6, 77, "padding", torch.bfloat16, torch.float32),
     (1000, 256, 256, 4, 1024, "distinct", torch.float16, torch.float16),

@@ -113,10 +113,10 @@ def test_embedding_refusals_before_any_launch(L):
 
 def test_embedding_backward_refusals_before_any_launch(L):
     f = L.flexq_embedding_backward
-    need = flexq.embedding_backward_workspace_bytes(400, 256)
+    need = flexq.embedding_backward_workspace_bytes(400, 100, 256)
     assert need > 0
-    assert flexq.embedding_backward_workspace_bytes(0, 256) == 0
-    assert flexq.embedding_backward_workspace_bytes(256, 256) == 0     # one launch, no scratch
+    assert flexq.embedding_backward_workspace_bytes(0, 100, 256) == 0
+    assert flexq.embedding_backward_workspace_bytes(256, 100, 256) == 0     # one launch, no scratch
     ok = dict(T=400, V=100, K=256, gs=128, bits=4, dtype=0, ids=FAKE, id_bytes=8, dY=FAKE, Wq=FAKE,
               scale=1.0, table_dtype=0, table=FAKE, scales=FAKE, ws=FAKE, ws_bytes=need,
               stream=NULL)

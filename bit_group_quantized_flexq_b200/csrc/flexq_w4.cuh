@@ -397,11 +397,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   float* xsum = reinterpret_cast<float*>(xs_mem + a.M * x_stride);        // [groups][8 NT tokens]
   float4* slab = reinterpret_cast<float4*>(xsum + (room * kGemvChunkCols >> a.gs_shift) * 8 * NT);  // [count][NT][32]
 
-  int first, count, units;          // the round's strips and this CTA's chunks of them
-  int u0, u1;                       // this warp's chunks
-  int c, strip;                     // of the chunk in hand
+  int first = 0, count = 0, units = 0;   // the round's strips and this CTA's chunks of them
+  int u0 = 0, u1 = 0;               // this warp's chunks
+  int c = 0, strip = 0;             // of the chunk in hand
   // the next chunk to request, its place in the share and in memory
-  int ru, rc, rs, asked = 0;
+  int ru = 0, rc = 0, rs = 0, asked = 0;
   const uint4* rp = nullptr;
   auto stream_at = [&](int strip, int c) {
     const int l = layer_of(strip);

@@ -226,8 +226,8 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
   if (rc) return rc;
   a.token_tiles = (a.M + T - 1) / T;
   const long long tiles = static_cast<long long>(a.tile0[L.n]) * a.token_tiles;
+  if (tiles * 8 > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d with so many weight rows is too large", a.M);
   a.split = w4_mma_split(tiles, a.kbs, static_cast<long long>(Cfg::kCtasPerSm) * sms);
-  if (tiles * a.split > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d with so many weight rows is too large", a.M);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
   cfg.blockDim = dim3(Cfg::kThreads);
@@ -243,8 +243,7 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
   cfg.attrs = attr;
   cfg.numAttrs = a.split > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, flexq::w4_mma_kernel<E, T, RB>, a);
-  if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
-  return FLEXQ_OK;
+  return e == cudaSuccess ? FLEXQ_OK : cuda_fail(e, "4-bit linear launch");
 }
 
 template <typename E>

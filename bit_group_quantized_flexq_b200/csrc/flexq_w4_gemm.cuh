@@ -304,19 +304,25 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
     const int q = warp & 3, h = (warp - 4) >> 2 & 1, rb = (warp - 4) >> 3;
     const int row = rb * 128 + q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    const int n_row = strip0 * 16 + row;        // of the layer
-    const bool in = n_row < a.N[l];
-    const unsigned short* sp = reinterpret_cast<const unsigned short*>(a.ws[l]) +
-                               static_cast<size_t>(in ? n_row : 0) * a.G;
-    // the scales of the groups of words 2 h and 2 h + 1 of tile i; one behind
-    // the last row or column is zero
-    auto scales = [&](int i, uint32_t (&s)[2]) {
-      const int k = (kb0 + i) * 128 + h * 64;
-      s[0] = s[1] = 0;
-      if (!in || i >= nk) return;
-      if (k < a.K) s[0] = __ldg(sp + (k >> a.gs_shift));
-      if (a.gs_shift >= 6) s[1] = s[0];
-      else if (k + 32 < a.K) s[1] = __ldg(sp + ((k + 32) >> a.gs_shift));
+    // Where the scales of words 2 h and 2 h + 1 of this row lie, for the even
+    // and the odd tiles: two tiles on is `step` scales on.  A row behind the
+    // last takes that one's (its sums are dropped).
+    const int n_row = min(strip0 * 16 + row, a.N[l] - 1), step = 256 >> a.gs_shift;
+    const unsigned short* sp[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      sp[j] = reinterpret_cast<const unsigned short*>(a.ws[l]) + static_cast<size_t>(n_row) * a.G +
+              (((kb0 + j) * 128 + h * 64) >> a.gs_shift);
+    const bool two = a.gs_shift < 6;            // words with a group each
+    // words of the last tile behind K have no scale (their codes are zeros)
+    const int last = a.kbs - kb0 - 1, last_words = (a.K - (a.kbs - 1) * 128 + 31) / 32 - 2 * h;
+    auto scales = [&](int i, int j, uint32_t (&s)[2]) {
+      const int words = i == last ? last_words : 2;
+      if (i < nk && words > 0) {
+        s[0] = s[1] = __ldg(sp[j]);
+        if (two && words > 1) s[1] = __ldg(sp[j] + 1);
+      }
+      sp[j] += step;
     };
     RingPos<Cfg::kWSlots> wp;
     uint32_t phase = 1;                         // of the A slots' release
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
 #pragma unroll
         for (int t = 0; t < 4; ++t) scale.apply(j == 0 ? c[t].x : c[t].y, out + 16 * j + 4 * t);
       }
-      scales(i + Cfg::kASlots, s);              // for this slot's next tile
+      scales(i + Cfg::kASlots, slot, s);        // for this slot's next tile
       if (!warp_wait(&a_empty[rb][slot], phase, lim)) return false;
       tc_fence_after();
       tmem_st32(lane_base + a_col0 + (slot * RB + rb) * Cfg::kACols + 32 * h, out);
@@ -348,9 +354,9 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
       if (lane == 0) mbar_arrive(&a_full[rb][slot]);
       return true;
     };
-    uint32_t s0[2], s1[2];
-    scales(0, s0);
-    scales(1, s1);
+    uint32_t s0[2] = {}, s1[2] = {};
+    scales(0, 0, s0);
+    scales(1, 1, s1);
     bool ok = true;
     static_assert(Cfg::kASlots == 2, "the loop below takes two tiles at a time");
     for (int i = 0; ok && i < nk; i += 2, phase ^= 1) {
@@ -436,15 +442,23 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
   for (int i = t0 * kPieces + threadIdx.x; i < t1 * kPieces; i += Cfg::kThreads) {
     const uint32_t at = smem_u32(base) + static_cast<uint32_t>(i) * 32;
     float sum[8] = {};
-    for (int r = 0; r < a.split; ++r) {
-      float v[8];
-      const uint32_t p = map_to_rank(at, r);
-      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(p) : "memory");
-      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "r"(p + 16) : "memory");
+    for (int r0 = 0; r0 < a.split; r0 += 4) {           // four ranks' sums in flight
+      float v[4][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      for (int r = 0; r < 4; ++r) {
+        if (r0 + r >= a.split) break;
+        const uint32_t p = map_to_rank(at, r0 + r);
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[r][0]), "=f"(v[r][1]), "=f"(v[r][2]), "=f"(v[r][3]) : "r"(p) : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[r][4]), "=f"(v[r][5]), "=f"(v[r][6]), "=f"(v[r][7]) : "r"(p + 16) : "memory");
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r0 + r >= a.split) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[r][j];
+      }
     }
     uint4 o;
     o.x = Elem<E>::pack(sum[0], sum[1]);

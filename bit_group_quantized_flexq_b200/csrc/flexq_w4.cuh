@@ -31,8 +31,9 @@ namespace flexq {
 // m16n8k16 MMA's A operand up to the order of k; that order is chosen so that
 // the lane's activations for one word are 16 contiguous bytes too.  The
 // nibble order puts consecutive columns into the two halves of a register
-// with one mask, and columns 0 .. 3 and 4 .. 7 into the same bits of them.  A row's 128 codes stay within 64 aligned bytes (two DRAM
-// sectors), so that rows can also be looked up alone.
+// with one mask, and columns 0 .. 3 and 4 .. 7 into the same bits of them.  A
+// row's 128 codes stay within 64 aligned bytes (two DRAM sectors), so that
+// rows can also be looked up alone.
 constexpr int kW4TileRows = 16;
 constexpr int kW4TileCols = 128;
 constexpr int kW4TileBytes = 1024;
@@ -227,9 +228,16 @@ struct W4Args {
   long long ldx;
   int M, K, G, kbs, gs_shift;     // kbs: tiles of 128 columns; gs = 1 << gs_shift
   int split, rounds;              // streaming kernel: CTAs of a cluster, parts of its strips
+  int stall;                      // test hook: every warp's first copy is withheld
   unsigned int* status;           // device status word
   unsigned long long wait_limit_ns;
 };
+
+// Brings bytes (a multiple of 16, 16-byte aligned) towards the L2 cache, where
+// what a kernel before writes into them meanwhile is seen too.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 
 // The product for batches of up to 16 tokens streams the weights once, so it
 // is bound by HBM; every SM must keep tens of KB of loads in flight from its
@@ -402,6 +410,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   int c = 0, strip = 0;             // of the chunk in hand
   // the next chunk to request, its place in the share and in memory
   int ru = 0, rc = 0, rs = 0, asked = 0;
+  bool ok = true;                   // no wait ran out
   const uint4* rp = nullptr;
   auto stream_at = [&](int strip, int c) {
     const int l = layer_of(strip);
@@ -410,7 +419,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   auto request = [&]() {
     if (ru >= u1) return;
     const bool end = rc + 1 == chunks;
-    if (lane == 0) {
+    if (lane == 0 && !(a.stall && asked == 0)) {
       const uint32_t bytes = (end ? end_tiles : kGemvChunk) * kW4TileBytes;
       mbar_arrive_expect_tx(&full[warp], bytes);
       bulk_load(buffer, rp, bytes, &full[warp]);
@@ -439,7 +448,6 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     rc = c = u0 % chunks;
     rs = strip = first + u0 / chunks;
     if (u0 < u1) rp = stream_at(strip, c);
-    request();
   };
   if (lane == 0) {
     mbar_init(&full[warp], 1);
@@ -448,6 +456,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   }
   __syncwarp();
   begin(0);
+  if (lane == 0 && u0 < u1) prefetch_l2(rp, (c + 1 == chunks ? end_tiles : kGemvChunk) * kW4TileBytes);
 
   // where the scales of rows g and g + 8 lie, from the next chunk on
   const bool even = a.K % kGemvChunkCols == 0;
@@ -468,22 +477,23 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     c0.load(p0, left0, even);
     c1.load(p1, left1, even);
   };
-  first_scales();
   // activations to shared memory; columns behind K are zeros
   const int padded = chunks * kGemvChunkCols;
   const int row_bytes = min(padded, a.K - c_lo * kGemvChunkCols) * 2, pad16 = (padded * 2 - row_bytes) / 16;
   for (int i = threadIdx.x; i < a.M * pad16; i += kGemvThreads)
     *reinterpret_cast<uint4*>(xs_mem + i / pad16 * x_stride + row_bytes + i % pad16 * 16) = make_uint4(0, 0, 0, 0);
   grid_launch_dependents();
-  grid_wait_dependencies();         // weights are constants; activations are not
+  grid_wait_dependencies();         // whatever the call reads may have been written just before
+  request();
   if (threadIdx.x == 0) {
     mbar_arrive_expect_tx(&x_full, a.M * row_bytes);
     for (int m = 0; m < a.M; ++m)
       bulk_load(xs_mem + m * x_stride, static_cast<const T*>(a.x) + m * a.ldx + c_lo * kGemvChunkCols,
                 row_bytes, &x_full);
   }
+  first_scales();
   __syncthreads();                  // x_full is initialised; the padding is written
-  bool ok = __syncthreads_and(mbar_wait(&x_full, 0, a.wait_limit_ns));
+  ok = __syncthreads_and(mbar_wait(&x_full, 0, a.wait_limit_ns));
   if (!ok && threadIdx.x == 0) record_status(a.status, kStatusTimeout, 2);
 
   // the sums of the activations of each token and group, gs / 8 lanes to a
@@ -625,6 +635,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   const int round_first = first, round_count = count;
   if (MANY && ++round < a.rounds) { // its first chunk comes while the sums are added
     begin(round);
+    if (ok) request();
     first_scales();
   }
   cluster_sync_all();

@@ -227,7 +227,8 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
   a.token_tiles = (a.M + T - 1) / T;
   const long long tiles = static_cast<long long>(a.tile0[L.n]) * a.token_tiles;
   if (tiles * 8 > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d with so many weight rows is too large", a.M);
-  a.split = w4_mma_split(tiles, a.kbs, static_cast<long long>(Cfg::kCtasPerSm) * sms);
+  a.first_wave = Cfg::kCtasPerSm * sms;
+  a.split = w4_mma_split(tiles, a.kbs, a.first_wave);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
   cfg.blockDim = dim3(Cfg::kThreads);
@@ -268,6 +269,7 @@ int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, i
   m.gs_shift = a.gs_shift;
   m.status = a.status;
   m.wait_limit_ns = a.wait_limit_ns;
+  m.stall = a.stall;
   // Two row blocks per CTA bring the activations half as often, once there are
   // tiles enough for a good part of the SMs: 28672 x 8192 at 64 tokens 53 us
   // with two and 68 with one, 11008 x 4096 at 256 tokens 30 and 34, but 1000 x
@@ -339,6 +341,7 @@ int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long l
   a.gs_shift = log2_gs(gs);
   a.status = st->status;
   a.wait_limit_ns = g_wait_limit_ns.load();
+  a.stall = g_inject_stall.exchange(0);
   // the kernels number the 16 x 128 tiles of a launch in 32 bits
   if (strips * a.kbs > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "%lld x %d weights are too many", strips * 16, K);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

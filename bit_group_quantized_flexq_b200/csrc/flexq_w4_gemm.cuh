@@ -39,6 +39,12 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z)
+               : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -124,9 +130,9 @@ struct RowScale<__nv_bfloat16> {
 
 template <int T, int RB>
 struct W4MmaCfg {
-  // Warps: 0 producer, 1 MMA, 2-3 idle, the others unpack and write the sums
-  // out, eight to a row block: two to a quarter of its rows with half a
-  // tile's columns each (with one, unpacking took longer than the MMAs).
+  // Warps: 0 producer, 1 .. RB MMA, idle up to 3; the others unpack and write
+  // the sums out, eight to a row block: two to a quarter of its rows with half
+  // a tile's columns each (with one, unpacking took longer than the MMAs).
   static constexpr int kUnpackWarps = 8 * RB;
   static constexpr int kThreads = 128 + 32 * kUnpackWarps;
   static constexpr int kCtasPerSm = 2 / RB;
@@ -165,6 +171,8 @@ struct W4MmaArgs {
   int M, K, G, kbs, gs_shift;
   int split;                            // CTAs of a cluster, which share a tile's columns
   int token_tiles;
+  int first_wave;                       // CTAs that start together
+  int stall;                            // test hook: the first tile is withheld
   unsigned int* status;
   unsigned long long wait_limit_ns;
 };
@@ -194,6 +202,19 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
   const int kb0 = static_cast<int>(static_cast<long long>(rank) * a.kbs / a.split);
   const int nk = static_cast<int>(static_cast<long long>(rank + 1) * a.kbs / a.split) - kb0;
 
+  auto load_w = [&](int i) {
+    if (a.stall && i == 0) return;
+    uint64_t* bar = &w_full[i % Cfg::kWSlots];
+    mbar_arrive_expect_tx(bar, Cfg::kWSlot);
+    tma_load_3d(w_mem + i % Cfg::kWSlots * Cfg::kWSlot, &a.w[l], bar, 0, (kb0 + i) * 16, strip0);
+  };
+  auto load_x = [&](int i) {
+    uint64_t* bar = &x_full[i % Cfg::kXSlots];
+    uint8_t* dst = x_mem + i % Cfg::kXSlots * Cfg::kXSlot;
+    mbar_arrive_expect_tx(bar, Cfg::kXSlot);
+    tma_load_2d(dst, &a.x, bar, (kb0 + i) * 128, mt * T);
+    tma_load_2d(dst + Cfg::kXBox, &a.x, bar, (kb0 + i) * 128 + 64, mt * T);
+  };
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < Cfg::kXSlots; ++i) {
       mbar_init(&x_full[i], 1);
@@ -211,22 +232,51 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
       mbar_init(&acc_full[rb], 1);
     }
     fence_barrier_init();
-  }
-  auto load_w = [&](int i) {
-    uint64_t* bar = &w_full[i % Cfg::kWSlots];
-    mbar_arrive_expect_tx(bar, Cfg::kWSlot);
-    tma_load_3d(w_mem + i % Cfg::kWSlots * Cfg::kWSlot, &a.w[l], bar, 0, (kb0 + i) * 16, strip0);
-  };
-  auto load_x = [&](int i) {
-    uint64_t* bar = &x_full[i % Cfg::kXSlots];
-    uint8_t* dst = x_mem + i % Cfg::kXSlots * Cfg::kXSlot;
-    mbar_arrive_expect_tx(bar, Cfg::kXSlot);
-    tma_load_2d(dst, &a.x, bar, (kb0 + i) * 128, mt * T);
-    tma_load_2d(dst + Cfg::kXBox, &a.x, bar, (kb0 + i) * 128 + 64, mt * T);
-  };
-  if (warp == 0 && lane == 0)           // the weights are constants: before the wait below
+    // towards L2 while the kernel before ends; its results are read behind the
+    // wait alone
+    if (static_cast<int>(blockIdx.x) < a.first_wave)
+      for (int i = 0; i < Cfg::kWSlots && i < nk; ++i) tma_prefetch_3d(&a.w[l], 0, (kb0 + i) * 16, strip0);
+    grid_wait_dependencies();
     for (int i = 0; i < Cfg::kWSlots && i < nk; ++i) load_w(i);
-  if (warp == 1) tmem_alloc(&tmem_at, Cfg::kTmemCols);
+    for (int i = 0; i < Cfg::kXSlots && i < nk; ++i) load_x(i);
+  }
+  // an unpack warp's quarter q of row block rb, and its half h of a tile's columns
+  const int q = warp & 3, h = (warp - 4) >> 2 & 1, rb = max(warp - 4, 0) >> 3;
+  const int row = rb * 128 + q * 32 + lane;
+  // Where the scales of words 2 h and 2 h + 1 of this row lie, for the even
+  // and the odd tiles: two tiles on is `step` scales on.  A row behind the
+  // last takes that one's (its sums are dropped).
+  const int n_row = min(strip0 * 16 + row, a.N[l] - 1), step = 256 >> a.gs_shift;
+  const unsigned short* sp[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    sp[j] = reinterpret_cast<const unsigned short*>(a.ws[l]) + static_cast<size_t>(n_row) * a.G +
+            (((kb0 + j) * 128 + h * 64) >> a.gs_shift);
+  const bool two = a.gs_shift < 6;              // words with a group each
+  // words of the last tile behind K have no scale (their codes are zeros)
+  const int last = a.kbs - kb0 - 1, last_words = (a.K - (a.kbs - 1) * 128 + 31) / 32 - 2 * h;
+  auto scales = [&](int i, int j, uint32_t (&s)[2]) {
+    const int words = i == last ? last_words : 2;
+    if (i < nk && words > 0) {
+      s[0] = s[1] = __ldg(sp[j]);
+      if (two && words > 1) s[1] = __ldg(sp[j] + 1);
+    }
+    sp[j] += step;
+  };
+  uint32_t s0[2] = {}, s1[2] = {};
+  if (warp >= 4) {
+    if (last > 0 || last_words > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(sp[0]));
+    grid_wait_dependencies();
+    scales(0, 0, s0);
+    scales(1, 1, s1);
+  }
+  // Tensor memory is taken after the kernel before has ended and before the
+  // next may begin: one that takes its own while others still wait for theirs
+  // would keep it until they end.
+  if (warp == 1) {
+    grid_wait_dependencies();
+    tmem_alloc(&tmem_at, Cfg::kTmemCols);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -237,8 +287,6 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
   if (warp == 0) {
     // ------------------------------------------------------- producer -----
     if (lane == 0) {
-      grid_wait_dependencies();
-      for (int i = 0; i < Cfg::kXSlots && i < nk; ++i) load_x(i);
       int w_issued = min(nk, Cfg::kWSlots), x_issued = min(nk, Cfg::kXSlots);
       bool ok = true;
       for (int i = 0; ok && i < nk; ++i) {
@@ -301,29 +349,7 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
     warp_wait(&acc_full[rb], 0, lim);
   } else if (warp >= 4) {
     // --------------------------------------------------------- unpack -----
-    const int q = warp & 3, h = (warp - 4) >> 2 & 1, rb = (warp - 4) >> 3;
-    const int row = rb * 128 + q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    // Where the scales of words 2 h and 2 h + 1 of this row lie, for the even
-    // and the odd tiles: two tiles on is `step` scales on.  A row behind the
-    // last takes that one's (its sums are dropped).
-    const int n_row = min(strip0 * 16 + row, a.N[l] - 1), step = 256 >> a.gs_shift;
-    const unsigned short* sp[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      sp[j] = reinterpret_cast<const unsigned short*>(a.ws[l]) + static_cast<size_t>(n_row) * a.G +
-              (((kb0 + j) * 128 + h * 64) >> a.gs_shift);
-    const bool two = a.gs_shift < 6;            // words with a group each
-    // words of the last tile behind K have no scale (their codes are zeros)
-    const int last = a.kbs - kb0 - 1, last_words = (a.K - (a.kbs - 1) * 128 + 31) / 32 - 2 * h;
-    auto scales = [&](int i, int j, uint32_t (&s)[2]) {
-      const int words = i == last ? last_words : 2;
-      if (i < nk && words > 0) {
-        s[0] = s[1] = __ldg(sp[j]);
-        if (two && words > 1) s[1] = __ldg(sp[j] + 1);
-      }
-      sp[j] += step;
-    };
     RingPos<Cfg::kWSlots> wp;
     uint32_t phase = 1;                         // of the A slots' release
     auto unpack = [&](int i, int slot, uint32_t (&s)[2]) -> bool {
@@ -354,9 +380,6 @@ __global__ void __launch_bounds__(W4MmaCfg<T, RB>::kThreads, W4MmaCfg<T, RB>::kC
       if (lane == 0) mbar_arrive(&a_full[rb][slot]);
       return true;
     };
-    uint32_t s0[2] = {}, s1[2] = {};
-    scales(0, 0, s0);
-    scales(1, 1, s1);
     bool ok = true;
     static_assert(Cfg::kASlots == 2, "the loop below takes two tiles at a time");
     for (int i = 0; ok && i < nk; i += 2, phase ^= 1) {

@@ -8,6 +8,10 @@ warp, 8 warps and 8 cluster ranks, each off by at most 2^-23 (a truncation) of
 the sum of magnitudes.  FP16 results below the normal range are off by half
 of 2^-24."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -166,6 +170,98 @@ def test_repeats_captured_and_on_another_stream(M):
     x.copy_(x2)
     graph.replay()
     check(out, x2, w64, torch.float16, gs)
+
+
+@pytest.mark.parametrize("M", [1, 12, 40, 300])
+def test_a_wait_that_runs_out_is_reported(M):
+    N, K, gs = 300, 2048, 128
+    wp, ws, w64 = packed(weights(N, K, 8), gs)
+    x = inputs.activations(M, K, seed=1)
+    assert flexq.device_status()[0] == flexq.FLEXQ_OK
+    flexq.set_wait_limit_ns(50_000_000)          # 50 ms
+    try:
+        flexq.inject_stall(True)
+        flexq.linear4(x.cuda(), wp, ws, N, gs)
+        status, msg = flexq.device_status()
+        assert status == flexq.FLEXQ_ERR_DEVICE_TIMEOUT, msg
+        assert flexq.device_status()[0] == flexq.FLEXQ_OK     # cleared
+    finally:
+        flexq.inject_stall(False)
+        flexq.set_wait_limit_ns(2_000_000_000)
+    check(flexq.linear4(x.cuda(), wp, ws, N, gs), x, w64, torch.float16, gs)
+    assert flexq.device_status()[0] == flexq.FLEXQ_OK
+
+
+FIRST_CALLS = """
+import torch
+from bit_group_quantized_flexq_b200 import flexq
+torch.manual_seed(0)
+w = torch.randn(400, 1024, device="cuda").half()
+wp, ws = flexq.quantize_weight4(w, 128)
+ids = torch.randint(-1, 400, (700,), device="cuda")
+xs = [torch.randn(m, 1024, device="cuda").half() for m in (1, 12, 40, 300)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    ys = [flexq.linear4(x, wp, ws, 400, 128) for x in xs]
+    e = flexq.embedding(ids, wp, ws, 400, 128)
+    rows, scales = flexq.embedding_backward(e, ids, wp, 400, 128, table_dtype=torch.float16)
+graph.replay()
+torch.cuda.synchronize()
+for x, y in zip(xs, ys):
+    assert torch.equal(y, flexq.linear4(x, wp, ws, 400, 128)), x.shape
+assert torch.equal(e, flexq.embedding(ids, wp, ws, 400, 128))
+again = flexq.embedding_backward(e, ids, wp, 400, 128, table_dtype=torch.float16)
+assert torch.equal(rows, again[0]) and torch.equal(scales, again[1])
+print("same")
+"""
+
+
+def test_first_calls_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True,
+                       timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_scales_written_just_before_are_the_ones_used():
+    # a step of scale tuning: the scales change in place between two products
+    N, K, gs = 700, 4096, 128
+    wp, ws, _ = packed(weights(N, K, 3), gs)
+    for M in (1, 12, 40, 300):
+        x = inputs.activations(M, K, seed=M).cuda()
+        s = ws.clone()
+        y = flexq.linear4(x, wp, s, N, gs)
+        for _ in range(4):
+            s.mul_(0.5)
+            half = flexq.linear4(x, wp, s, N, gs)
+            # halving is exact down to subnormal results
+            assert torch.allclose(half.float() * 2, y.float(), rtol=2.0 ** -9, atol=2.0 ** -22)
+            y = half
+
+
+def test_codes_written_just_before_are_the_ones_used():
+    # weights exchanged in place between two products, eagerly and replayed
+    N, K, gs = 700, 4096, 128
+    wa, ws, _ = packed(weights(N, K, 3), gs)
+    wb, _, _ = packed(weights(N, K, 4), gs)
+    for M in (1, 12, 40, 300):
+        x = inputs.activations(M, K, seed=M).cuda()
+        want = [flexq.linear4(x, w, ws, N, gs) for w in (wa, wb)]
+        assert not torch.equal(*want)
+        w = wa.clone()
+        graph = torch.cuda.CUDAGraph()
+        got = []
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            for i in range(8):
+                w.copy_((wb, wa)[i % 2])
+                got.append(flexq.linear4(x, w, ws, N, gs))
+        graph.replay()
+        for i, y in enumerate(got):
+            assert torch.equal(y, want[(i + 1) % 2]), (M, i)
+        for i in range(8):
+            w.copy_((wb, wa)[i % 2])
+            assert torch.equal(flexq.linear4(x, w, ws, N, gs), want[(i + 1) % 2]), (M, i)
 
 
 def test_refusals_on_the_gpu():

@@ -433,7 +433,7 @@ cudaError_t launch_sums(const flexq::Table& tb, flexq::SumArgs a, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t sum = cudaLaunchKernelEx(&cfg, flexq::embed_sum_kernel<T, TO, BITS>, tb, a);
-  if (sum != cudaSuccess || tiles == 1) return sum;
+  if (sum != cudaSuccess) return sum;           // more than kFewTokens make several tiles
   cfg.gridDim = dim3(tiles, pieces);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, flexq::embed_join_kernel<T, TO, BITS>, tb, a);

@@ -403,9 +403,12 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
 /*
  * flexq_linear_w4 -- Y = X . dequant(Wq)^T with 4-bit weights.
  *   dtype      FLEXQ_DTYPE_FP16 or FLEXQ_DTYPE_BF16: the type of X and Y.
- *   X, ldx     [M, K], rows ldx elements apart (ldx >= K, ldx % 8 == 0).
+ *   X, ldx     [M, K], rows ldx elements apart (ldx >= K, ldx % 8 == 0), finite
+ *              values; one that is not leaves no value of its token finite, and
+ *              the other tokens alone.
  *   Y, ldy     out, [M, N], rows ldy >= N elements apart; nothing between the
- *              rows is written.  Y needs its elements' alignment only.
+ *              rows is written.  Y needs its elements' alignment only, and must
+ *              not overlap X.
  * Y[m,n] = round(sum_g s[n,g] * sum_{k in g} X[m,k] q[n,k]), sums in FP32,
  * rounded once, for batches of at most 16 tokens of moderate K
  * (flexq_linear_w4_exact).  Larger ones multiply weights that are rounded to

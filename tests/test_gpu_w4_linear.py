@@ -264,6 +264,22 @@ def test_codes_written_just_before_are_the_ones_used():
             assert torch.equal(flexq.linear4(x, w, ws, N, gs), want[(i + 1) % 2]), (M, i)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("M", [2, 16, 40, 300])
+def test_a_token_that_is_not_finite_stays_alone(M, dtype):
+    N, K, gs = 300, 1024, 64
+    wp, ws, w64 = packed(weights(N, K, 8), gs)
+    x = inputs.activations(M, K, seed=2).to(dtype)
+    want = flexq.linear4(x.cuda(), wp, ws, N, gs)
+    for m, value in ((0, float("nan")), (M - 1, float("inf"))):
+        bad = x.clone()
+        bad[m, 700] = value
+        y = flexq.linear4(bad.cuda(), wp, ws, N, gs)
+        assert not torch.isfinite(y[m]).any()
+        rest = [i for i in range(M) if i != m]
+        assert torch.equal(y[rest], want[rest])
+
+
 def test_refusals_on_the_gpu():
     wp, ws, _ = packed(weights(16, 256, 1), 128)
     x = torch.zeros(4, 256, dtype=torch.float16, device="cuda")

@@ -103,8 +103,8 @@ __device__ __forceinline__ int token_row(const void* ids, int id_bytes, long lon
 // Bound by writing the rows: 16 bytes a thread, consecutive threads write
 // consecutive pieces.  A thread keeps its columns and takes kLookAhead tokens
 // at a time, so that their ids, then their codes and scales, are in flight
-// together.  Measured: 16384 tokens x 8192 from 4 bits 64 to 72 us, 4.2 to 4.7
-// TB/s where a fill of that size alone reaches 4; 4096 tokens x 4096 from 6 bits
+// together.  Measured: 16384 tokens x 8192 from 4 bits 64 to 72 us, 4.1 to 4.6
+// TB/s, where zeros alone are filled in at 4 to 5; 4096 tokens x 4096 from 6 bits
 // 16.4; one token 1.7.
 constexpr int kLookThreads = 256;
 constexpr int kLookCols = kLookThreads * 8;
@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(kLookThreads) embed_kernel(const Table tb, con
 // other clusters meanwhile zero the scales' gradient and what of the rows'
 // they can in that time; the rest of it, but for the rows with a token, is
 // zeroed beside the sums.  Bound by latency: 8192 tokens of 32000 rows take two
-// passes, 17 us in all, most of it the cluster's barriers and the chain from a
-// token's digit to its place; a sort of one CTA takes twice that, and one of all
-// CTAs would meet at a barrier that costs as much as a pass.
+// passes and 17 us, the chain of digit counts, barriers and places of each; the
+// 64 MB of zeros take 12 of them.  More CTAs than a cluster holds would meet in
+// global memory.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortDigits = 256;

@@ -100,25 +100,27 @@ __device__ __forceinline__ int token_row(const void* ids, int id_bytes, long lon
 }
 
 // ------------------------------------------------------------------ lookup --
-// Bound by writing the rows: 16 bytes a thread, consecutive threads write
-// consecutive pieces.  A thread keeps its columns and takes kLookAhead tokens
-// at a time, so that their ids, then their codes and scales, are in flight
-// together.  Measured: 16384 tokens x 8192 from 4 bits 64 to 72 us, 4.1 to 4.6
-// TB/s, where zeros alone are filled in at 4 to 5; 4096 tokens x 4096 from 6 bits
-// 16.4; one token 1.7.
+// Bound by writing the rows: 16 bytes a thread, consecutive threads and then
+// consecutive CTAs write consecutive pieces.  A thread keeps its columns and takes
+// a few tokens at a time, so that their ids, then their codes and scales, are in
+// flight together: four with 4 bits (16384 tokens x 8192 take 62 us, with two 69),
+// two with 6, whose codes are three words (4096 tokens x 4096 15.4 us, with four
+// 16.3).  62 us are 4.7 TB/s; asking for the next tokens' ids meanwhile costs more
+// in registers than it hides (66 to 76 us).  One token takes 1.7 us.
 constexpr int kLookThreads = 256;
 constexpr int kLookCols = kLookThreads * 8;
-constexpr int kLookAhead = 4;
+__host__ __device__ constexpr int look_ahead(int bits) { return bits == 4 ? 4 : 2; }
 
 template <typename T, int BITS>
 __global__ void __launch_bounds__(kLookThreads) embed_kernel(const Table tb, const void* __restrict__ ids,
                                                              int id_bytes, int tokens, float scale,
                                                              T* __restrict__ out) {
-  const int k = blockIdx.y * kLookCols + threadIdx.x * 8;
+  constexpr int kLookAhead = look_ahead(BITS);
+  const int k = blockIdx.x * kLookCols + threadIdx.x * 8;   // consecutive CTAs write a row's pieces
   if (k >= tb.K) return;
   const int grp = k >> tb.gs_shift;
-  for (long long t0 = static_cast<long long>(blockIdx.x) * kLookAhead; t0 < tokens;
-       t0 += static_cast<long long>(gridDim.x) * kLookAhead) {
+  for (long long t0 = static_cast<long long>(blockIdx.y) * kLookAhead; t0 < tokens;
+       t0 += static_cast<long long>(gridDim.y) * kLookAhead) {
     int v[kLookAhead];
 #pragma unroll
     for (int j = 0; j < kLookAhead; ++j)
@@ -141,8 +143,11 @@ __global__ void __launch_bounds__(kLookThreads) embed_kernel(const Table tb, con
         const float f = __half2float(s[j]);
         uint32_t* p = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)      // code * scale is exact in FP32
-          p[i] = Elem<T>::pack(q[2 * i] * f * scale, q[2 * i + 1] * f * scale);
+        for (int i = 0; i < 4; ++i) {    // code * scale is exact in FP32
+          const float2 x = __fmul2_rn(__fmul2_rn(make_float2(q[2 * i], q[2 * i + 1]), make_float2(f, f)),
+                                      make_float2(scale, scale));
+          p[i] = Elem<T>::pack(x.x, x.y);
+        }
       }
       __stcs(reinterpret_cast<uint4*>(out + static_cast<size_t>(t0 + j) * tb.K + k), o);
     }
@@ -157,9 +162,8 @@ __global__ void __launch_bounds__(kLookThreads) embed_kernel(const Table tb, con
 // other clusters meanwhile zero the scales' gradient and what of the rows'
 // they can in that time; the rest of it, but for the rows with a token, is
 // zeroed beside the sums.  Bound by latency: 8192 tokens of 32000 rows take two
-// passes and 17 us, the chain of digit counts, barriers and places of each; the
-// 64 MB of zeros take 12 of them.  More CTAs than a cluster holds would meet in
-// global memory.
+// passes and 17 us, the chain of digit counts, barriers and places of each.  More
+// CTAs than a cluster holds would meet in global memory.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortDigits = 256;
@@ -414,8 +418,8 @@ __device__ __forceinline__ void async_wait() {
 // registers instead, a wait for one token's waited for the next ones' too:
 // 16384 tokens x 8192 took 100 us for 66.)  The zeros of the rows without a
 // token are written by CTAs in between: 8192 tokens and 32000 x 4096 BF16 rows
-// take 79 us in all three launches, FP32 rows 118, where the zeros alone are 262
-// and 524 MB at 4 to 5 TB/s.
+// take 73 us in all three launches, FP32 rows 108; the bytes alone (262 or 524
+// MB of rows, 67 of dY) are 51 and 91 us at a copy's rate.
 template <int BITS>
 struct SumRing {
   static constexpr int kStages = 6;

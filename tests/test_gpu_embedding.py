@@ -202,6 +202,18 @@ def test_scale_gradient_against_differences():
         assert abs(diff - float(scales[v, g])) <= float(err) * 2.0 ** -11 / step + 1e-5
 
 
+@pytest.mark.parametrize("bits", [4, 6])
+def test_lookup_of_more_tokens_than_a_launch_takes_at_once(bits):
+    V, K, gs = 128, 256, 64
+    wp, ws, q, s = table(V, K, gs, bits)
+    ids = torch.randint(-1, V + 1, (100003,), generator=torch.Generator().manual_seed(5))
+    y = flexq.embedding(ids.cuda(), wp, ws, V, gs, weight_bits=bits)
+    rows = (q.astype(np.float32) * np.repeat(s.astype(np.float32), gs, axis=1)).astype(np.float16)
+    rows = np.concatenate([rows, np.zeros((1, K), np.float16)])
+    at = np.where((ids.numpy() >= 0) & (ids.numpy() < V), ids.numpy(), V)
+    assert np.array_equal(y.cpu().numpy(), rows[at])
+
+
 def test_captured_and_replayed_beside_another_stream():
     V, K, gs, T = 500, 1024, 128, 3000
     wp, ws, q, s = table(V, K, gs, 4)

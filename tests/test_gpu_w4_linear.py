@@ -172,6 +172,25 @@ def test_repeats_captured_and_on_another_stream(M):
     check(out, x2, w64, torch.float16, gs)
 
 
+def test_calls_on_two_streams_at_once():
+    N, K, gs = 3000, 4096, 128
+    wp, ws, _ = packed(weights(N, K, 8), gs)
+    xs = [inputs.activations(m, K, seed=m).cuda() for m in (1, 12, 40, 300)]
+    want = [flexq.linear4(x, wp, ws, N, gs) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        # the streams go through the batches in opposite directions
+        for turn, stream in ((i, streams[0]), (3 - i, streams[1])):
+            with torch.cuda.stream(stream):
+                got.append((turn % 4, flexq.linear4(xs[turn % 4], wp, ws, N, gs)))
+    torch.cuda.synchronize()
+    for m, y in got:
+        assert torch.equal(y, want[m])
+    assert flexq.device_status()[0] == flexq.FLEXQ_OK
+
+
 @pytest.mark.parametrize("M", [1, 12, 40, 300])
 def test_a_wait_that_runs_out_is_reported(M):
     N, K, gs = 300, 2048, 128

@@ -749,25 +749,27 @@ def embedding_backward(dy, ids, wp, V, group_size, scale=1.0, weight_bits=4, tab
     if table_dtype is None:
         table = None
     elif table is None:
-        table = torch.empty((V, K), dtype=table_dtype, device=dy.device)
+        table = dy.new_empty((V, K), dtype=table_dtype)
     elif not _is(table, table_dtype, (V, K), dev):
         _refuse(table, "rows", table_dtype, (V, K), dy)
     shape = _scales_shape(V, K, group_size, weight_bits)
     if not with_scales:
         scales = None
     elif scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=dy.device)
+        scales = dy.new_empty(shape, dtype=torch.float32)
     elif not _is(scales, torch.float32, shape, dev):
         _refuse(scales, "scales", torch.float32, shape, dy)
     if workspace_buf is None:
-        workspace_buf = torch.empty(embedding_backward_workspace_bytes(T, V, K), dtype=torch.uint8,
-                                    device=dy.device)
-    elif not _is(workspace_buf, torch.uint8, (workspace_buf.numel(),), dev):
-        _refuse(workspace_buf, "workspace", torch.uint8, (workspace_buf.numel(),), dy)
+        need = lib().flexq_embedding_backward_workspace_bytes(T, V, K)
+        space = dy.new_empty(need, dtype=torch.uint8) if need else None    # none for few tokens
+    else:
+        space, need = workspace_buf, workspace_buf.numel()
+        if not _is(space, torch.uint8, (need,), dev):
+            _refuse(space, "workspace", torch.uint8, (need,), dy)
     _launch(dev, lib().flexq_embedding_backward, T, V, K, group_size, weight_bits, _DTYPES[dtype],
             ids.data_ptr(), id_bytes, dy.data_ptr(), wp.data_ptr(), scale,
             _DTYPES[table_dtype] if table is not None else 0,
             None if table is None else table.data_ptr(),
-            None if scales is None else scales.data_ptr(), workspace_buf.data_ptr(),
-            workspace_buf.numel())
+            None if scales is None else scales.data_ptr(),
+            None if space is None else space.data_ptr(), need)
     return table, scales

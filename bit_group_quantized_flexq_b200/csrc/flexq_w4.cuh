@@ -116,9 +116,10 @@ struct Elem<__half> {
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
           "f"(c[2]), "f"(c[3]));
   }
-  // The eight codes of a word as exact FP16 pairs of consecutive columns.  A
-  // nibble in the low mantissa bits of 1024 is 1024 + u; four bits further up
-  // it is 1024 + 16 u, brought down by an exact multiply-add.
+  // The eight codes of a word as exact FP16 pairs of consecutive columns, by
+  // the common way of putting an integer's bits into the mantissa of a power
+  // of two: a nibble in the low mantissa bits of 1024 is 1024 + u; four bits
+  // further up it is 1024 + 16 u, brought down by an exact multiply-add.
   static __device__ __forceinline__ void codes(uint32_t w, uint32_t (&p)[4]) {
     const __half2 off = __half2half2(__ushort_as_half(0x6408));      // 1032
     const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));   // 1/16
@@ -136,19 +137,9 @@ struct Elem<__half> {
     o[2] = __hfma2(h[1], sixteenth, off16);
     o[3] = __hfma2(h[3], sixteenth, off16);
   }
-  // The same without the subtraction, for a product corrected by the sum of
-  // the activations: u in the lowest mantissa bits of a subnormal (columns
-  // 0 .. 3, u * 2^-24), or four bits up (4 .. 7, 16 u * 2^-24).  Exact.
-  static constexpr float kOffset = 8.0f / 16777216.0f;     // of columns 0 .. 3
-  static constexpr float kHigh = 1.0f / 16.0f;             // columns 4 .. 7 to their unit
-  static constexpr float kUnit = 16777216.0f;
-  static __device__ __forceinline__ void offset_codes(uint32_t w, uint32_t (&p)[4]) {
-    const uint32_t v = w >> 8;
-    p[0] = w & 0x000F000Fu;
-    p[1] = v & 0x000F000Fu;
-    p[2] = w & 0x00F000F0u;
-    p[3] = v & 0x00F000F0u;
-  }
+  // The streaming kernel's operand: the codes as they are.
+  static constexpr float kUnit = 1.0f;
+  static __device__ __forceinline__ void operand(uint32_t w, uint32_t (&p)[4]) { codes(w, p); }
 };
 
 template <>
@@ -172,27 +163,23 @@ struct Elem<__nv_bfloat16> {
           "f"(c[2]), "f"(c[3]));
   }
   // BF16 has 7 mantissa bits: a nibble in the low ones of 128 is 128 + u; the
-  // other nibbles are shifted there first.
+  // other nibbles are shifted there first.  DOWN: in units of 2^-DOWN.
+  template <int DOWN = 0>
   static __device__ __forceinline__ void codes(uint32_t w, uint32_t (&p)[4]) {
-    const __nv_bfloat162 off = __bfloat162bfloat162(__ushort_as_bfloat16(0x4308));   // 136
+    constexpr uint32_t base = 0x4300u - (DOWN << 7);                           // 128
+    const __nv_bfloat162 off = __bfloat162bfloat162(__ushort_as_bfloat16(base + 8));   // 136
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t b = and_or(w >> w4_shift(2 * i), 0x000F000Fu, 0x43004300u);
+      const uint32_t b = and_or(w >> w4_shift(2 * i), 0x000F000Fu, base << 16 | base);
       const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), off);
       p[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
-  // Without the subtraction: u in the upper four mantissa bits of 16 is
-  // 16 + u = q + 24.  (In a subnormal it would leave the sums no precision.)
-  static constexpr float kOffset = 24.0f;
-  static constexpr float kHigh = 1.0f;
-  static constexpr float kUnit = 1.0f;
-  static __device__ __forceinline__ void offset_codes(uint32_t w, uint32_t (&p)[4]) {
-    p[0] = and_or(w << 3, 0x00780078u, 0x41804180u);
-    p[1] = and_or(w >> 5, 0x00780078u, 0x41804180u);
-    p[2] = and_or(w >> 1, 0x00780078u, 0x41804180u);
-    p[3] = and_or(w >> 9, 0x00780078u, 0x41804180u);
-  }
+  // The streaming kernel's operand: codes in units of 2^-11, so that a group's
+  // sum, of at most 256 terms of at most 8 |x|, is at most the largest |x| and
+  // no finite activation overflows it.
+  static constexpr float kUnit = 2048.0f;
+  static __device__ __forceinline__ void operand(uint32_t w, uint32_t (&p)[4]) { codes<11>(w, p); }
 };
 
 // ---------------------------------------------------- matrix-vector product --
@@ -243,22 +230,24 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
 // rounds.
 //
 // Taking a code apart has to cost little: at HBM's rate an SM has about 44
-// cycles per tile.  So the tensor core multiplies codes with an offset, u = q
-// + 8 (in units that differ by type), which takes one mask each, and a group's
-// product starts from minus the offset times the sum of its activations,
-// which every CTA forms once while its first weights are on the way.
+// cycles per tile.  Yet the tensor core multiplies the signed codes, 9 (FP16)
+// and 11 (BF16) instructions per word: multiplying u = q + 8 and starting a
+// group from -8 times the sum of its activations takes 5, but those sums
+// cancel, so that a large activation on a zero code costs all other terms of
+// its group bits.  (That way one token x 28672 x 8192 took 25.8 us, 8 x 8192 x
+// 8192 13.1 and 16 x 4096 x 4096 11.1, for 27.9, 12.2 and 7.3: the sums of the
+// activations have their price too.)
 //
-// Measured (device time, weights cold): 28672 x 8192 at one token 25.8 us, 4.7
-// TB/s or 0.72 of a copy's rate; the same kernel without its arithmetic takes
+// Measured (device time, weights cold): 28672 x 8192 at one token 27.9 us, 4.3
+// TB/s or 0.66 of a copy's rate; the same kernel without its arithmetic takes
 // 21.4 us.  Between the two is the time from a chunk's arrival to the next
-// request, with the four warps that a scheduler has: it issues in half of its
-// cycles, ALU 39 % and tensor core 23 % busy.  20 and 24 warps took 27.1 and
-// 30.7 us, chunks of two tiles 33, a ring of three 31.  4096 x 4096 takes 5.3
-// us, of which its stream is 1.3: launch, the first bytes and the final sums
-// are the rest.
-// 16 tokens x 28672 columns take 55 us: a lane reads its activations from
+// request, with the four warps that a scheduler has.  20 and 24 warps take 29.7
+// and 33.3 us, chunks of two tiles 30.6.  4096 x 4096 takes 5.2 us, of which
+// its stream is 1.3: launch, the first bytes and the final sums are the rest.
+// 16 tokens x 28672 columns take 51 us: a lane reads its activations from
 // shared memory four times as often as its codes, and 15 clusters of eight,
-// which is what their activations need, fill 120 of 148 SMs.
+// which is what their activations need, fill 120 of 148 SMs.  (Chunks of two
+// tiles take 44.6 there, but 5 to 10 % more at one token.)
 constexpr int kGemvWarps = 16;
 constexpr int kGemvThreads = kGemvWarps * 32;
 constexpr int kGemvChunk = 4;                 // tiles
@@ -309,20 +298,27 @@ struct ChunkScales {
 
 // acc += one 16 x 128 tile times the activations of 8 NT tokens.  x: the
 // lane's activations of the chunk, those of the n-th eight tokens xo[n] bytes
-// on; c0, c1: scales of rows g and g + 8; xs: for each group of the chunk,
-// minus the codes' offset times the sum of the activations of tokens 2 t and
-// 2 t + 1; WPG: words (of 32 columns) per group, 8 where a group is two tiles.
+// on; c0, c1: scales of rows g and g + 8; WPG: words (of 32 columns) per
+// group, 8 where a group is two tiles.
+//
+// Two chains of MMAs are in flight: of the words' halves where there is one
+// eight of tokens and a group has several words, else one for each eight (two
+// words' halves then cost their addition per group and registers: 16 tokens x
+// 28672 columns 53.1 us with them and 51.0 without, 5 tokens x 32003 x 4096 in
+// groups of 64 17.6 and 16.9; one token x 28672 x 8192 in groups of 128 27.6
+// and 28.0).
 template <typename T, int WPG, int NS, int NT>
 __device__ __forceinline__ void gemv_tile(float (&acc)[NT][4], const uint4& w0, const uint4& w1,
                                           const uint8_t* x, const int (&xo)[NT],
                                           const ChunkScales<NS>& c0,
-                                          const ChunkScales<NS>& c1, const float* xs, int tile) {
-  float lower[NT][4], upper[NT][4];     // columns 0 .. 3 and 4 .. 7 of the words
+                                          const ChunkScales<NS>& c1, int tile) {
+  constexpr bool kHalves = NT == 1 && WPG >= 4;
+  float sum[NT][4], upper[4];           // upper: columns 4 .. 7 of the words, where they are apart
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t lo[4], hi[4];
-    Elem<T>::offset_codes(reinterpret_cast<const uint32_t*>(&w0)[j], lo);
-    Elem<T>::offset_codes(reinterpret_cast<const uint32_t*>(&w1)[j], hi);
+    Elem<T>::operand(reinterpret_cast<const uint32_t*>(&w0)[j], lo);
+    Elem<T>::operand(reinterpret_cast<const uint32_t*>(&w1)[j], hi);
     const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
     const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
     const int i = (tile * 4 + j) / WPG;
@@ -330,21 +326,17 @@ __device__ __forceinline__ void gemv_tile(float (&acc)[NT][4], const uint4& w0, 
     for (int n = 0; n < NT; ++n) {
       const uint4 xv = *reinterpret_cast<const uint4*>(x + xo[n] + tile * 256 + j * 64);
       if (j % WPG == 0) {
-        float2 o = make_float2(0.0f, 0.0f);         // the second tile of a group goes on
-        if (WPG <= 4 || tile % 2 == 0) o = *reinterpret_cast<const float2*>(xs + 8 * NT * i + 8 * n);
-        const float from[4] = {o.x, o.y, o.x, o.y}, zero[4] = {};
-        Elem<T>::mma(lower[n], a0, xv.x, xv.y, from);
-        Elem<T>::mma(upper[n], a1, xv.z, xv.w, zero);
-      } else {
-        Elem<T>::mma(lower[n], a0, xv.x, xv.y, lower[n]);
-        Elem<T>::mma(upper[n], a1, xv.z, xv.w, upper[n]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[n][e] = upper[e] = 0.0f;
       }
+      Elem<T>::mma(sum[n], a0, xv.x, xv.y, sum[n]);
+      if (kHalves) Elem<T>::mma(upper, a1, xv.z, xv.w, upper);
+      else Elem<T>::mma(sum[n], a1, xv.z, xv.w, sum[n]);
       if ((j + 1) % WPG == 0 || j == 3) {
         const float f0 = c0.get(i), f1 = c1.get(i);
-        acc[n][0] = fmaf(fmaf(upper[n][0], Elem<T>::kHigh, lower[n][0]), f0, acc[n][0]);
-        acc[n][1] = fmaf(fmaf(upper[n][1], Elem<T>::kHigh, lower[n][1]), f0, acc[n][1]);
-        acc[n][2] = fmaf(fmaf(upper[n][2], Elem<T>::kHigh, lower[n][2]), f1, acc[n][2]);
-        acc[n][3] = fmaf(fmaf(upper[n][3], Elem<T>::kHigh, lower[n][3]), f1, acc[n][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[n][e] = fmaf(kHalves ? sum[n][e] + upper[e] : sum[n][e], e < 2 ? f0 : f1, acc[n][e]);
       }
     }
   }
@@ -363,11 +355,10 @@ __host__ __device__ constexpr int gemv_x_stride(int chunks) { return chunks * kG
 // Eights of tokens that the kernel multiplies at once.
 __host__ __device__ constexpr int gemv_eights(int M) { return M <= 8 ? 1 : 2; }
 
-// Shared memory: the warps' buffers, the activations, their sums per group,
-// and with a cluster the sums of the strips of a round.
-__host__ __device__ constexpr long long gemv_smem(int M, int kbs, int gs_shift, int split, int strips) {
+// Shared memory: the warps' buffers, the activations, and with a cluster the
+// sums of the strips of a round.
+__host__ __device__ constexpr long long gemv_smem(int M, int kbs, int split, int strips) {
   return kGemvBufferBytes + static_cast<long long>(M) * gemv_x_stride(gemv_share(kbs, split)) +
-         (static_cast<long long>(gemv_share(kbs, split)) * kGemvChunkCols >> gs_shift) * gemv_eights(M) * 32 +
          (split > 1 ? static_cast<long long>(strips) * gemv_eights(M) * 512 : 0);
 }
 
@@ -401,8 +392,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   const int room = gemv_share(kbs, a.split), x_stride = gemv_x_stride(room);
   uint8_t* buffer = buffers + warp * kGemvChunkBytes;
   uint8_t* xs_mem = buffers + kGemvBufferBytes;                           // [M][x_stride]
-  float* xsum = reinterpret_cast<float*>(xs_mem + a.M * x_stride);        // [groups][8 NT tokens]
-  float4* slab = reinterpret_cast<float4*>(xsum + (room * kGemvChunkCols >> a.gs_shift) * 8 * NT);  // [count][NT][32]
+  float4* slab = reinterpret_cast<float4*>(xs_mem + a.M * x_stride);      // [count][NT][32]
 
   int first = 0, count = 0, units = 0;   // the round's strips and this CTA's chunks of them
   int u0 = 0, u1 = 0;               // this warp's chunks
@@ -495,21 +485,6 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
   ok = __syncthreads_and(mbar_wait(&x_full, 0, a.wait_limit_ns));
   if (!ok && threadIdx.x == 0) record_status(a.status, kStatusTimeout, 2);
 
-  // the sums of the activations of each token and group, gs / 8 lanes to a
-  // group; behind K they are zero like the scales there
-  const int vecs = padded / 8;      // a multiple of 64
-  for (int i = threadIdx.x; i < a.M * vecs; i += kGemvThreads) {
-    const int m = i / vecs, k = (i - m * vecs) * 8;
-    const uint4 v = *reinterpret_cast<const uint4*>(xs_mem + m * x_stride + k * 2);
-    const float2 q0 = Elem<T>::unpack(v.x), q1 = Elem<T>::unpack(v.y);
-    const float2 q2 = Elem<T>::unpack(v.z), q3 = Elem<T>::unpack(v.w);
-    float sum = ((q0.x + q0.y) + (q1.x + q1.y)) + ((q2.x + q2.y) + (q3.x + q3.y));
-#pragma unroll
-    for (int o = 2 * WPG; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane % (4 * WPG) == 0) xsum[(k >> a.gs_shift) * 8 * NT + m] = -Elem<T>::kOffset * sum;
-  }
-  __syncthreads();
-
   // a column of the product without a token is computed and dropped
   const uint8_t* x = xs_mem + min(g, a.M - 1) * x_stride + t * 16;
   int xo[NT];
@@ -573,15 +548,14 @@ __global__ void __launch_bounds__(kGemvThreads, 1) w4_gemv_kernel(const __grid_c
     __syncwarp();                   // every lane holds the chunk
     request();                      // the next one comes while this one is multiplied
     const uint8_t* xp = x + c * (kGemvChunkCols * 2);
-    const float* xs = xsum + c * NS * 8 * NT + 2 * t;
     if (!end || end_tiles == kGemvChunk) {
 #pragma unroll
       for (int i = 0; i < kGemvChunk; ++i)
-        gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, xo, c0, c1, xs, i);
+        gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, xo, c0, c1, i);
     } else {
 #pragma unroll
       for (int i = 0; i < kGemvChunk; ++i)
-        if (i < end_tiles) gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, xo, c0, c1, xs, i);
+        if (i < end_tiles) gemv_tile<T, WPG, NS, NT>(acc, w[i][0], w[i][1], xp, xo, c0, c1, i);
     }
     c0 = n0;
     c1 = n1;

@@ -97,10 +97,10 @@ cudaError_t gemv_clusters(int sms, const int (*&clusters)[4]) {
 
 // Whether the streaming kernel takes a batch: by its size, and by whether the
 // share of its activations of some cluster's CTA fits shared memory.
-bool gemv_takes(int M, int kbs, int gs_shift) {
+bool gemv_takes(int M, int kbs) {
   if (M > kGemvTokens || kbs > (1 << 13)) return false;
   for (int s = 1; s <= 8 && s <= flexq::gemv_chunks(kbs); s *= 2)
-    if (flexq::gemv_smem(M, kbs, gs_shift, s, 1) <= gemv_smem_limit(M)) return true;
+    if (flexq::gemv_smem(M, kbs, s, 1) <= gemv_smem_limit(M)) return true;
   return false;
 }
 
@@ -121,8 +121,8 @@ bool gemv_plan(const flexq::W4Args& a, int strips, const int (&clusters)[4], Gem
     const int most = (strips + n - 1) / n, share = flexq::gemv_share(a.kbs, s);
     int rounds = 1;
     auto of_a_round = [&] { return (most + rounds - 1) / rounds; };
-    while (rounds < most && flexq::gemv_smem(a.M, a.kbs, a.gs_shift, s, of_a_round()) > room) ++rounds;
-    const long long smem = flexq::gemv_smem(a.M, a.kbs, a.gs_shift, s, of_a_round());
+    while (rounds < most && flexq::gemv_smem(a.M, a.kbs, s, of_a_round()) > room) ++rounds;
+    const long long smem = flexq::gemv_smem(a.M, a.kbs, s, of_a_round());
     if (smem > room) continue;
     const long long units = static_cast<long long>(most) * share + (rounds - 1) * 2 * flexq::kGemvWarps;
     if (units > INT32_MAX || (best >= 0 && units >= best)) continue;
@@ -249,7 +249,7 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
 
 template <typename E>
 int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, int sms, cudaStream_t s) {
-  if (gemv_takes(a.M, a.kbs, a.gs_shift)) {
+  if (gemv_takes(a.M, a.kbs)) {
     return flexq::gemv_eights(a.M) == 1 ? launch_gemv_gs<E, 1>(gs, L, a, sms, s)
                                         : launch_gemv_gs<E, 2>(gs, L, a, sms, s);
   }
@@ -480,7 +480,7 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
 
 int flexq_linear_w4_exact(int M, int K, int group_size) {
   if (M <= 0 || check_w4_shape(1, K, group_size)) return 0;
-  return gemv_takes(M, flexq::w4_col_tiles(K), log2_gs(group_size)) ? 1 : 0;
+  return gemv_takes(M, flexq::w4_col_tiles(K)) ? 1 : 0;
 }
 
 int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,

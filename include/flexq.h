@@ -409,7 +409,8 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
  *   Y, ldy     out, [M, N], rows ldy >= N elements apart; nothing between the
  *              rows is written.  Y needs its elements' alignment only, and must
  *              not overlap X.
- * Y[m,n] = round(sum_g s[n,g] * sum_{k in g} X[m,k] q[n,k]), sums in FP32,
+ * Y[m,n] = round(sum_g s[n,g] * sum_{k in g} X[m,k] q[n,k]), sums in FP32 of
+ * the products themselves (a group's does not overflow for any finite X),
  * rounded once, for batches of at most 16 tokens of moderate K
  * (flexq_linear_w4_exact).  Larger ones multiply weights that are rounded to
  * dtype: Y[m,n] = round(sum_k X[m,k] round(s[n,g] q[n,k])), infinite where 7 s

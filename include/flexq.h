@@ -413,8 +413,10 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
  * the products themselves (a group's does not overflow for any finite X),
  * rounded once, for batches of at most 16 tokens of moderate K
  * (flexq_linear_w4_exact).  Larger ones multiply weights that are rounded to
- * dtype: Y[m,n] = round(sum_k X[m,k] round(s[n,g] q[n,k])), infinite where 7 s
- * exceeds FP16's range.  The summation order depends on the shapes alone.
+ * dtype: Y[m,n] = round(sum_k X[m,k] round(s[n,g] q[n,k])).  Every weight of
+ * flexq_quantize_weight4 stays finite there (7 times its largest scale, 9360,
+ * is taken as FP16's largest value, within half a step; scales above that may
+ * give infinite FP16 weights).  The summation order depends on the shapes alone.
  */
 int flexq_linear_w4_exact(int M, int K, int group_size);
 int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,

@@ -501,9 +501,10 @@ def linear_group(x, weights, group_size, act_bits=6, outs=None, workspace_buf=No
 # word a refusal.
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _LAYER4 = struct.Struct("@i4xPPPq").pack     # flexq_layer4_t
-_Tensor, _raw_stream, _cur_device = (torch.Tensor, torch._C._cuda_getCurrentRawStream,
-                                     torch._C._cuda_getDevice) if torch.cuda.is_available() else \
-    (torch.Tensor, None, None)
+# names only: an import must not initialise CUDA (forked workers could not use it then)
+_Tensor = torch.Tensor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _is(t, dtype, shape, dev):

@@ -50,7 +50,6 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<unsigned long long>& 
   return e;
 }
 
-template <typename T, int WPG, int NT>
 cudaLaunchConfig_t gemv_config(unsigned ctas, int split, size_t smem, cudaLaunchAttribute (&attr)[2],
                                cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -70,37 +69,44 @@ cudaLaunchConfig_t gemv_config(unsigned ctas, int split, size_t smem, cudaLaunch
   return cfg;
 }
 
-// Clusters of 1, 2, 4 and 8 CTAs that run at once, one CTA per SM (asked once
-// per device; 0 where the driver has no place for any).
-template <typename T, int WPG, int NT>
-cudaError_t gemv_clusters(int sms, const int (*&clusters)[4]) {
+// Clusters of 1, 2, 4 and 8 CTAs with an SM each that the current device runs at
+// once, asked once per device; 0 where it has no place for any (a part of a GPU
+// may not).  The streaming kernels all take one CTA per SM.
+std::atomic<int> g_cluster_limit{8};     // test hook: larger ones are taken as not available
+
+cudaError_t device_clusters(int sms, int (&clusters)[4]) {
   static int known[kMaxDevices][4];
+  static std::atomic<unsigned long long> ready{0};
+  const auto kern = flexq::w4_gemv_kernel<__half, 4, 1, false>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = allow_smem(kern, gemv_smem_limit(8), ready);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   if (known[dev][0] == 0) {
     int n[4] = {sms, 0, 0, 0};
     for (int i = 1; i < 4; ++i) {
       cudaLaunchAttribute attr[2];
-      cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(1u << i, 1 << i, gemv_smem_limit(8 * NT), attr, nullptr);
+      cudaLaunchConfig_t cfg = gemv_config(1u << i, 1 << i, gemv_smem_limit(8), attr, nullptr);
       cfg.attrs = attr + 1;
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&n[i], flexq::w4_gemv_kernel<T, WPG, NT, false>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n[i], kern, &cfg);
       if (e != cudaSuccess) return e;
     }
     memcpy(known[dev], n, sizeof(n));
   }
-  clusters = &known[dev];
+  const int limit = g_cluster_limit.load();
+  for (int i = 0; i < 4; ++i) clusters[i] = 1 << i <= limit ? known[dev][i] : 0;
   return cudaSuccess;
 }
 
 // Whether the streaming kernel takes a batch: by its size, and by whether the
-// share of its activations of some cluster's CTA fits shared memory.
-bool gemv_takes(int M, int kbs) {
+// share of its activations of a CTA fits shared memory in some cluster that the
+// device has.
+bool gemv_takes(int M, int kbs, const int (&clusters)[4]) {
   if (M > kGemvTokens || kbs > (1 << 13)) return false;
-  for (int s = 1; s <= 8 && s <= flexq::gemv_chunks(kbs); s *= 2)
-    if (flexq::gemv_smem(M, kbs, s, 1) <= gemv_smem_limit(M)) return true;
+  for (int i = 0; i < 4 && 1 << i <= flexq::gemv_chunks(kbs); ++i)
+    if (clusters[i] > 0 && flexq::gemv_smem(M, kbs, 1 << i, 1) <= gemv_smem_limit(M)) return true;
   return false;
 }
 
@@ -133,14 +139,12 @@ bool gemv_plan(const flexq::W4Args& a, int strips, const int (&clusters)[4], Gem
 }
 
 template <typename T, int WPG, int NT>
-int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, int sms, cudaStream_t stream) {
+int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, const int (&clusters)[4], cudaStream_t stream) {
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem(flexq::w4_gemv_kernel<T, WPG, NT, false>, gemv_smem_limit(8 * NT), ready);
-  const int (*clusters)[4] = nullptr;
-  if (e == cudaSuccess) e = gemv_clusters<T, WPG, NT>(sms, clusters);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit linear set-up");
   GemvPlan p;
-  if (!gemv_plan(a, L.strip0[L.n], *clusters, &p))
+  if (!gemv_plan(a, L.strip0[L.n], clusters, &p))
     return fail(FLEXQ_ERR_UNSUPPORTED, "no launch for %d tokens, %d strips, K=%d", a.M, L.strip0[L.n], a.K);
   a.split = p.split;
   a.rounds = p.rounds;
@@ -150,19 +154,20 @@ int launch_gemv(const flexq::W4Layers& L, flexq::W4Args a, int sms, cudaStream_t
     if (e != cudaSuccess) return cuda_fail(e, "4-bit linear set-up");
   }
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = gemv_config<T, WPG, NT>(static_cast<unsigned>(p.clusters * p.split), p.split,
-                                                         static_cast<size_t>(p.smem), attr, stream);
+  const cudaLaunchConfig_t cfg = gemv_config(static_cast<unsigned>(p.clusters * p.split), p.split,
+                                             static_cast<size_t>(p.smem), attr, stream);
   e = p.rounds == 1 ? cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG, NT, false>, L, a)
                     : cudaLaunchKernelEx(&cfg, flexq::w4_gemv_kernel<T, WPG, NT, true>, L, a);
   return e == cudaSuccess ? FLEXQ_OK : cuda_fail(e, "4-bit linear launch");
 }
 
 template <typename T, int NT>
-int launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, int sms, cudaStream_t stream) {
-  return gs == 32    ? launch_gemv<T, 1, NT>(L, a, sms, stream)
-         : gs == 64  ? launch_gemv<T, 2, NT>(L, a, sms, stream)
-         : gs == 128 ? launch_gemv<T, 4, NT>(L, a, sms, stream)
-                     : launch_gemv<T, 8, NT>(L, a, sms, stream);
+int launch_gemv_gs(int gs, const flexq::W4Layers& L, const flexq::W4Args& a, const int (&clusters)[4],
+                   cudaStream_t stream) {
+  return gs == 32    ? launch_gemv<T, 1, NT>(L, a, clusters, stream)
+         : gs == 64  ? launch_gemv<T, 2, NT>(L, a, clusters, stream)
+         : gs == 128 ? launch_gemv<T, 4, NT>(L, a, clusters, stream)
+                     : launch_gemv<T, 8, NT>(L, a, clusters, stream);
 }
 
 // ---- batches beyond those: the tcgen05 kernel ----
@@ -203,16 +208,17 @@ int encode_w4_map(CUtensorMap* map, const void* wp, int N, int kbs, int strips) 
 
 // CTAs of a cluster that share a tile's columns: as many as still run in one
 // wave (a sixteenth of the machine's places is left, as clusters do not fill
-// every group of SMs), each with at least four column tiles.
-int w4_mma_split(long long tiles, int kbs, long long slots) {
+// every group of SMs), each with at least four column tiles; `most` is the
+// largest cluster that the device has.
+int w4_mma_split(long long tiles, int kbs, long long slots, int most) {
   int split = 1;
-  while (split < 8 && tiles * (split + 1) <= slots * 15 / 16 && kbs >= 4 * (split + 1)) ++split;
+  while (split < most && tiles * (split + 1) <= slots * 15 / 16 && kbs >= 4 * (split + 1)) ++split;
   return split;
 }
 
 template <typename E, int T, int RB>
 int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, long long ldx, int sms,
-                  cudaStream_t stream) {
+                  int most, cudaStream_t stream) {
   using Cfg = flexq::W4MmaCfg<T, RB>;
   constexpr int dtype = std::is_same<E, __half>::value ? FLEXQ_DTYPE_FP16 : FLEXQ_DTYPE_BF16;
   static std::atomic<unsigned long long> ready{0};
@@ -228,7 +234,7 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
   const long long tiles = static_cast<long long>(a.tile0[L.n]) * a.token_tiles;
   if (tiles * 8 > INT32_MAX) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d with so many weight rows is too large", a.M);
   a.first_wave = Cfg::kCtasPerSm * sms;
-  a.split = w4_mma_split(tiles, a.kbs, a.first_wave);
+  a.split = w4_mma_split(tiles, a.kbs, a.first_wave, most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
   cfg.blockDim = dim3(Cfg::kThreads);
@@ -249,10 +255,15 @@ int launch_w4_mma(flexq::W4MmaArgs& a, const flexq::W4Layers& L, const void* x, 
 
 template <typename E>
 int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, int sms, cudaStream_t s) {
-  if (gemv_takes(a.M, a.kbs)) {
-    return flexq::gemv_eights(a.M) == 1 ? launch_gemv_gs<E, 1>(gs, L, a, sms, s)
-                                        : launch_gemv_gs<E, 2>(gs, L, a, sms, s);
+  int clusters[4], most = 1;
+  const cudaError_t e = device_clusters(sms, clusters);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit linear set-up");
+  if (gemv_takes(a.M, a.kbs, clusters)) {
+    return flexq::gemv_eights(a.M) == 1 ? launch_gemv_gs<E, 1>(gs, L, a, clusters, s)
+                                        : launch_gemv_gs<E, 2>(gs, L, a, clusters, s);
   }
+  for (int i = 1; i < 4; ++i)
+    if (clusters[i] > 0) most = 1 << i;
   flexq::W4MmaArgs m;
   memset(&m, 0, sizeof(m));
   m.n = L.n;
@@ -279,13 +290,13 @@ int launch_linear_w4(const flexq::W4Layers& L, const flexq::W4Args& a, int gs, i
   for (int l = 0; l < L.n; ++l) tiles += (L.N[l] + 255) / 256;
   const bool two = T >= 32 && tiles * ((a.M + T - 1) / T) * 5 >= sms;
   switch (T) {
-    case 16: return launch_w4_mma<E, 16, 1>(m, L, a.x, a.ldx, sms, s);
-    case 32: return two ? launch_w4_mma<E, 32, 2>(m, L, a.x, a.ldx, sms, s)
-                        : launch_w4_mma<E, 32, 1>(m, L, a.x, a.ldx, sms, s);
-    case 64: return two ? launch_w4_mma<E, 64, 2>(m, L, a.x, a.ldx, sms, s)
-                        : launch_w4_mma<E, 64, 1>(m, L, a.x, a.ldx, sms, s);
-    default: return two ? launch_w4_mma<E, 128, 2>(m, L, a.x, a.ldx, sms, s)
-                        : launch_w4_mma<E, 128, 1>(m, L, a.x, a.ldx, sms, s);
+    case 16: return launch_w4_mma<E, 16, 1>(m, L, a.x, a.ldx, sms, most, s);
+    case 32: return two ? launch_w4_mma<E, 32, 2>(m, L, a.x, a.ldx, sms, most, s)
+                        : launch_w4_mma<E, 32, 1>(m, L, a.x, a.ldx, sms, most, s);
+    case 64: return two ? launch_w4_mma<E, 64, 2>(m, L, a.x, a.ldx, sms, most, s)
+                        : launch_w4_mma<E, 64, 1>(m, L, a.x, a.ldx, sms, most, s);
+    default: return two ? launch_w4_mma<E, 128, 2>(m, L, a.x, a.ldx, sms, most, s)
+                        : launch_w4_mma<E, 128, 1>(m, L, a.x, a.ldx, sms, most, s);
   }
 }
 
@@ -480,7 +491,21 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
 
 int flexq_linear_w4_exact(int M, int K, int group_size) {
   if (M <= 0 || check_w4_shape(1, K, group_size)) return 0;
-  return gemv_takes(M, flexq::w4_col_tiles(K)) ? 1 : 0;
+  int clusters[4] = {1, 1, 1, 1}, n = 0;      // without a device, those of a whole GPU
+  DeviceState* st = nullptr;
+  if (cudaGetDeviceCount(&n) != cudaSuccess || n == 0) {
+    cudaGetLastError();
+    for (int i = 0; i < 4; ++i) clusters[i] = 1 << i <= g_cluster_limit.load();
+  } else if (device_state(&st) || device_clusters(st->sms, clusters) != cudaSuccess) {
+    return 0;
+  }
+  return gemv_takes(M, flexq::w4_col_tiles(K), clusters) ? 1 : 0;
+}
+
+int flexq_debug_limit_clusters(int most) {
+  if (most < 0 || most > 8) return fail(FLEXQ_ERR_INVALID_ARG, "most=%d is not in 0..8", most);
+  g_cluster_limit.store(most == 0 ? 8 : most);
+  return ok();
 }
 
 int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,

@@ -95,6 +95,7 @@ def lib():
             "flexq_debug_force_linear_route": (c_int, [c_int]),
             "flexq_set_wait_limit_ns": (c_int, [ctypes.c_uint64]),
             "flexq_debug_inject_stall": (c_int, [c_int]),
+            "flexq_debug_limit_clusters": (c_int, [c_int]),
             "flexq_get_device_status": (c_int, [c_void_p]),
             "flexq_quantize_weight_layout": (c_int, [c_int, c_int, c_int, c_int, c_void_p,
                                                      c_void_p, c_void_p, c_void_p]),
@@ -410,6 +411,12 @@ def inject_stall(enable=True):
     _check(lib().flexq_debug_inject_stall(1 if enable else 0))
 
 
+def limit_clusters(most=0):
+    """Test hook: the 4-bit products take clusters of more than `most` CTAs as
+    not available; 0 restores the device's."""
+    _check(lib().flexq_debug_limit_clusters(most))
+
+
 def device_status(device=None):
     """Synchronizes the current stream and returns (status, message); clears it."""
     s = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
@@ -626,8 +633,9 @@ def _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out):
 
 
 def linear4_exact(M, K, group_size):
-    """Whether linear4 multiplies the codes themselves for a batch of M tokens;
-    larger batches round the dequantized weights to x's type first."""
+    """Whether linear4 multiplies the codes themselves for a batch of M tokens
+    on the current device; larger batches round the dequantized weights to x's
+    type first."""
     return bool(lib().flexq_linear_w4_exact(M, K, group_size))
 
 

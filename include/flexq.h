@@ -412,7 +412,8 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
  * Y[m,n] = round(sum_g s[n,g] * sum_{k in g} X[m,k] q[n,k]), sums in FP32 of
  * the products themselves (a group's does not overflow for any finite X),
  * rounded once, for batches of at most 16 tokens of moderate K
- * (flexq_linear_w4_exact).  Larger ones multiply weights that are rounded to
+ * (flexq_linear_w4_exact says it for the current device, or for a whole B200
+ * where there is none).  Larger ones multiply weights that are rounded to
  * dtype: Y[m,n] = round(sum_k X[m,k] round(s[n,g] q[n,k])).  Every weight of
  * flexq_quantize_weight4 stays finite there (7 times its largest scale, 9360,
  * is taken as FP16's largest value, within half a step; scales above that may
@@ -564,6 +565,13 @@ int flexq_set_wait_limit_ns(uint64_t limit_ns);
  * flexq_get_device_status() and leave the context usable.  One-shot.
  */
 int flexq_debug_inject_stall(int enable);
+
+/*
+ * flexq_debug_limit_clusters -- test hook: the 4-bit products of this process
+ * take thread-block clusters of more than `most` CTAs (1..8) as not available,
+ * as on a part of a GPU that has no place for them.  0 restores the device's.
+ */
+int flexq_debug_limit_clusters(int most);
 
 /*
  * flexq_get_device_status -- synchronizes `stream`, reads the current

@@ -306,6 +306,8 @@ int linear_w4_common(int M, int K, int gs, int dtype, const void* X, long long l
     return fail(FLEXQ_ERR_INVALID_ARG, "n_layers=%d is not in 1..%d", n_layers, flexq::kW4MaxLayers);
   if (!layers) return fail(FLEXQ_ERR_INVALID_ARG, "layers is NULL");
   if (M < 0) return fail(FLEXQ_ERR_INVALID_ARG, "M=%d is negative", M);
+  // a tile of 128 tokens may number 127 behind the last one
+  if (M > INT32_MAX - 127) return fail(FLEXQ_ERR_UNSUPPORTED, "M=%d too large", M);
   int rc = check_dtype(dtype);
   if (rc) return rc;
   for (int l = 0; l < n_layers; ++l)

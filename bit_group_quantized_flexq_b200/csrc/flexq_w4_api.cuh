@@ -395,8 +395,9 @@ void launch_embed(int bits, const flexq::Table& tb, const void* ids, int id_byte
     flexq::embed_kernel<T, 6><<<grid, flexq::kLookThreads, 0, s>>>(tb, ids, id_bytes, tokens, scale, static_cast<T*>(out));
 }
 
-// Sorted tokens per CTA: about six CTAs per SM where there are that many
-// tokens, between 16 (below, runs that several tiles share cost more than the
+// Sorted tokens per CTA: about six CTAs for each of a whole GPU's 148 SMs (and
+// not the device's own number, so that sums have one order everywhere and the
+// workspace's size needs no device) where there are that many tokens, between 16 (below, runs that several tiles share cost more than the
 // CTAs bring) and kSumMaxTile.
 int sum_tile(long long T, int K) {
   const long long cols = (K + 2 * flexq::kSumCols - 1) / (2 * flexq::kSumCols);

@@ -11,17 +11,21 @@
 // than an SM receives in them.  An unpacked weight is the rounded product of
 // code and scale, half a step of the activations' type: keeping the codes whole
 // and scaling each group's sum instead would read the accumulator back once per
-// group, which costs a tile of 128 tokens more time than its MMAs.
+// group, which costs a tile of 128 tokens more time than its MMAs, and a second
+// MMA for the rounding's rest would take as long as the first.  The error of a
+// result grows from that of its own rounding, 0.0017 in BF16 and 0.00021 in FP16
+// of the result's root mean square, to 0.0023 and 0.00027.
 //
 // With fewer tiles than the machine has room for, a cluster of CTAs shares a
 // tile's columns; each leaves its sums in its shared memory, and the CTAs add
 // them up in the order of the columns, a share of the tokens each.
 //
-// Bound by unpacking: 13 instructions per word of eight codes in FP16, 20 in
-// BF16, and about as many around them (waits, addresses, scales), at 0.66
+// Bound by unpacking: 13 instructions per word of eight codes in FP16, 19 in
+// BF16, and about as many around them (waits, addresses, scales), at 0.65
 // instructions per cycle and scheduler.  Measured (device time): 11008 x 4096 at
-// 32 tokens 15.5 us, at 256 30 us (BF16 33), at 2048 150 us, 1235 TFLOP/s;
-// 28672 x 8192 at 64 tokens 51 us.  A warp's time per tile does not fall with
+// 32 tokens 15.8 us, at 256 30.4 us (BF16 33.9), at 2048 152 us, 1215 TFLOP/s, in
+// short runs and 176 us, 1050, in a long one that meets the power cap; 28672 x
+// 8192 at 64 tokens 53 us.  A warp's time per tile does not fall with
 // fewer warps beside it (tiles of 160 rows, which fill 138 SMs at 256 tokens
 // where those of 256 fill 86: 31.5 and 33.8 us), nor with three slots of
 // unpacked weights for two; leaving the wait for a tile's stores until the next

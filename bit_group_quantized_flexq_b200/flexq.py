@@ -504,8 +504,9 @@ def linear_group(x, weights, group_size, act_bits=6, outs=None, workspace_buf=No
 
 # ------------------------------------------- 4-bit layers and packed tables --
 # These calls are short enough for the host's time to matter: arguments are
-# checked in one expression each, and taken apart (_need, _need_rows) only to
-# word a refusal.
+# checked in one expression each, and taken apart (_refuse, _refuse_rows) only
+# to word a refusal.  Like the 6-bit calls they are outside autograd: results
+# carry no gradient, whatever their inputs; embedding_backward is called by hand.
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _LAYER4 = struct.Struct("@i4xPPPq").pack     # flexq_layer4_t
 # names only: an import must not initialise CUDA (forked workers could not use it then)
@@ -586,7 +587,8 @@ def _w4_bytes(N, K, group_size, what):
 
 def quantize_weight4(w, group_size, out=None):
     """FP16 W [N, K] -> (packed 4-bit codes, uint8 [weight4_packed_bytes(N, K,
-    gs)], FP16 scales [N, K/gs]).  Any N; K a multiple of the group size."""
+    gs)], FP16 scales [N, K/gs]).  Any N; K a multiple of the group size.  W of
+    another type is converted by the caller."""
     _need(w, "w", torch.float16)
     if w.dim() != 2:
         raise ValueError(f"w must be [N, K], got {tuple(w.shape)}")
@@ -635,7 +637,7 @@ def _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out):
 def linear4_exact(M, K, group_size):
     """Whether linear4 multiplies the codes themselves for a batch of M tokens
     on the current device; larger batches round the dequantized weights to x's
-    type first."""
+    type first (or are given in pieces, as views of their rows, to avoid it)."""
     return bool(lib().flexq_linear_w4_exact(M, K, group_size))
 
 
@@ -643,7 +645,7 @@ def linear4(x, wp, ws, N, group_size, out=None):
     """Y [M, N] of a layer with 4-bit weights (quantize_weight4) from FP16 or
     BF16 activations x [M, K], which are not quantized; Y has x's type.  x and
     out may be views whose rows lie further apart (x: by a multiple of eight
-    elements)."""
+    elements), and must not overlap.  Y carries no gradient."""
     code, dtype, dev, M, K, ldx = _w4_input(x)
     y, ldy = _w4_layer(x, wp, ws, N, group_size, M, K, dtype, dev, out)
     _launch(dev, lib().flexq_linear_w4, M, N, K, group_size, code, x.data_ptr(), ldx,
@@ -701,7 +703,8 @@ def embedding(ids, wp, ws, V, group_size, scale=1.0, weight_bits=4, dtype=torch.
     """Rows of a packed table [V, K]: out[..., :] = scale * dequantized row of
     each token of ids (int32 or int64, any shape), in FP16 or BF16.  wp, ws:
     quantize_weight4 (weight_bits 4) or quantize_weight (6, byte-aligned
-    layout).  A token outside [0, V) is padding: its row is zero."""
+    layout).  A token outside [0, V) is padding: its row is zero.  The result
+    carries no gradient: embedding_backward forms it from the result's."""
     dev, id_bytes = _check_ids(ids)
     if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")

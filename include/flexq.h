@@ -409,15 +409,18 @@ int flexq_quantize_weight4(int N, int K, int group_size, const void* W_fp16, voi
  *   Y, ldy     out, [M, N], rows ldy >= N elements apart; nothing between the
  *              rows is written.  Y needs its elements' alignment only, and must
  *              not overlap X.
- * Y[m,n] = round(sum_g s[n,g] * sum_{k in g} X[m,k] q[n,k]), sums in FP32 of
- * the products themselves (a group's does not overflow for any finite X),
- * rounded once, for batches of at most 16 tokens of moderate K
- * (flexq_linear_w4_exact says it for the current device, or for a whole B200
- * where there is none).  Larger ones multiply weights that are rounded to
- * dtype: Y[m,n] = round(sum_k X[m,k] round(s[n,g] q[n,k])).  Every weight of
+ * Batches of at most 16 tokens of moderate K: Y[m,n] = round(sum_g s[n,g] *
+ * sum_{k in g} X[m,k] q[n,k]), sums in FP32 of the products themselves (a
+ * group's does not overflow for any finite X), rounded once.
+ * flexq_linear_w4_exact says whether a batch is one of these on the current
+ * device, or on a whole B200 where there is none.
+ * Larger batches multiply weights that are rounded to dtype: Y[m,n] =
+ * round(sum_k X[m,k] round(s[n,g] q[n,k])).  Every weight of
  * flexq_quantize_weight4 stays finite there (7 times its largest scale, 9360,
  * is taken as FP16's largest value, within half a step; scales above that may
- * give infinite FP16 weights).  The summation order depends on the shapes alone.
+ * give infinite FP16 weights).  A caller who wants the first form gives such a
+ * batch in pieces.
+ * The summation order depends on the shapes and the device alone.
  */
 int flexq_linear_w4_exact(int M, int K, int group_size);
 int flexq_linear_w4(int M, int N, int K, int group_size, int dtype, const void* X, long long ldx,
@@ -442,7 +445,8 @@ int flexq_linear_w4_group(int M, int K, int group_size, int dtype, const void* X
 
 /*
  * flexq_embedding -- rows of a packed table: out[t,:] = scale * q[id_t,:] *
- * s[id_t, group], each value rounded once to dtype.
+ * s[id_t, group], each value formed in FP32 (q * s exactly, the product with
+ * scale rounded there) and then rounded to dtype.
  *   T, ids, id_bytes  T tokens, int32 (id_bytes 4) or int64 (8), aligned to
  *                     their size.  A token outside [0, V) is padding: its row
  *                     is zero.
